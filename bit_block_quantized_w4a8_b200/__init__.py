@@ -29,6 +29,8 @@ __all__ = [
     "w4a8_grouped_gemm_i32", "w4a8_grouped_gemm_schedule", "w4a8_gemm_variant", "VARIANTS",
     "w4a8_gemm_fused", "w4a8_gemm_fused_supported", "w4a8_gemm_kernel_kind",
     "KERNEL_TENSOR_CORE", "KERNEL_WARP_MMA", "w4a8_debug_set_wait_budget",
+    "w4a8_moe_route", "w4a8_moe_dispatch", "w4a8_moe_combine", "MoEDispatch",
+    "w4a8_lora", "w4a8_lora_plan", "LoraPlan",
 ]
 
 OK = 0
@@ -51,6 +53,11 @@ VARIANTS = {"default": 0, "baseline": 1, "naive_dequant": 2, "serial": 3, "one_g
 # kernels behind w4a8_gemm (W4A8_KERNEL_* in include/w4a8.h)
 KERNEL_TENSOR_CORE = 0
 KERNEL_WARP_MMA = 1
+
+# element types and routing scores (W4A8_TYPE_*, W4A8_SCORE_* in include/w4a8.h)
+_TYPES = {_torch.float32: 0, _torch.bfloat16: 1}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+LORA_IDS_MAX = 256  # rows that w4a8_lora groups by itself
 
 
 class W4A8Error(RuntimeError):
@@ -100,6 +107,14 @@ def lib():
             "w4a8_gemm_variant": ([i32, p, p, p, i32, i32, i32, p, p, _ct.c_uint, p], i32),
             "w4a8_gemm_fused": ([p, p, i32, i32, i32, p, _ct.c_uint, p], i32),
             "w4a8_gemm_fused_supported": ([i32, i32, i32], i32),
+            "w4a8_moe_route": ([p, i32, i32, i32, i32, i32, p, i32, i32, i32, i32, _ct.c_float,
+                                p, p, _ct.c_uint, p], i32),
+            "w4a8_moe_dispatch": ([p, i32, i32, i32, p, i32, i32, p, p, p, p, p, _ct.c_uint, p],
+                                  i32),
+            "w4a8_moe_combine": ([p, i32, i32, p, p, i32, i32, p, i32, _ct.c_uint, p], i32),
+            "w4a8_lora_plan": ([p, i32, i32, p, p, _ct.c_uint, p], i32),
+            "w4a8_lora": ([p, i32, ll, i32, i32, p, p, i32, i32, p, p, p, p, i32, p, ll,
+                           _ct.c_uint, p], i32),
             "w4a8_get_status": ([p], i32),
             "w4a8_debug_timeout_probe": ([ll, p], i32),
             "w4a8_debug_set_wait_budget": ([ll], i32),
@@ -430,6 +445,230 @@ def w4a8_gemm_fused(X, packed, out=None, stream=None, flags=0):
     Y = _out(out, _torch.bfloat16, (M, packed.N), X, "out")
     _check(lib().w4a8_gemm_fused(_ptr(X), _ptr(packed.data), M, packed.N, K, _ptr(Y),
                                  int(flags), _stream(stream)), "w4a8_gemm_fused")
+    return Y
+
+
+def _typed(t, ndim, name):
+    """The element type code of a contiguous fp32 or bf16 CUDA tensor."""
+    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    code = _TYPES.get(t.dtype)
+    if code is None or t.dim() != ndim or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous %dD float32 or bfloat16 tensor" % (name, ndim))
+    return code
+
+
+def _together(stream, first, *others):
+    """All tensors on one device, which has to be the current one (the
+    kernels are launched there), and the stream's handle."""
+    d = first.device
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError("tensors on %s and %s" % (d, t.device))
+    if d.index != _torch.cuda.current_device():
+        raise ValueError("tensors on %s, but the current device is cuda:%d"
+                         % (d, _torch.cuda.current_device()))
+    if stream is not None and stream.device != d:
+        raise ValueError("tensors on %s, stream on %s" % (d, stream.device))
+    return _stream(stream)
+
+
+def _new(stream, shape, dtype, device):
+    """A tensor for a call to write on its stream: it comes from that stream's
+    own memory, so nothing that ran on the current stream still uses it."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
+
+
+def w4a8_moe_route(logits, top_k, score="softmax", bias=None, groups=1, top_groups=1,
+                   group_top=1, renormalize=True, scale=1.0, ids=None, weights=None,
+                   stream=None, flags=0):
+    """Experts of each token: router logits [M, E] (fp32 or bf16) -> (ids int32
+    [M, top_k], weights fp32 [M, top_k]), best first.
+
+    ``score`` is "softmax" or "sigmoid"; ``bias`` fp32 [E] takes part in the
+    choice only; with ``groups`` > 1 only the experts of the ``top_groups``
+    best groups are open, a group counting for its best (``group_top`` = 1) or
+    its two best (2) experts.  ``renormalize`` divides the weights by their
+    sum, then ``scale`` multiplies them.  Ties go to the lowest index; masked
+    experts (-inf, NaN or the lowest bf16 value and below) are never chosen,
+    and slots that nothing is left for have id -1 and weight 0."""
+    kind = _typed(logits, 2, "logits")
+    M, E = logits.shape
+    k = int(top_k)
+    if score not in _SCORES:
+        raise ValueError("score must be one of %s" % sorted(_SCORES))
+    if bias is not None:
+        _need(bias, _torch.float32, 1, "bias")
+        if bias.numel() != E:
+            raise ValueError("bias has %d entries for %d experts" % (bias.numel(), E))
+    if k < 1:
+        raise ValueError("top_k must be positive")
+    st = _together(stream, logits, bias)
+    ids = (_new(stream, (M, k), _torch.int32, logits.device) if ids is None
+           else _out(ids, _torch.int32, (M, k), logits, "ids"))
+    weights = (_new(stream, (M, k), _torch.float32, logits.device) if weights is None
+               else _out(weights, _torch.float32, (M, k), logits, "weights"))
+    _check(lib().w4a8_moe_route(_ptr(logits), kind, M, E, k, _SCORES[score], _ptr(bias),
+                                int(groups), int(top_groups), int(group_top),
+                                1 if renormalize else 0, float(scale), _ptr(ids), _ptr(weights),
+                                int(flags), st), "w4a8_moe_route")
+    return ids, weights
+
+
+class MoEDispatch:
+    """Tokens grouped by expert: rows ``Xq`` int8 [M * k, K] with scales ``s_x``
+    [M * k], the experts' ``offsets`` int32 [E + 1] (as w4a8_grouped_gemm takes
+    them), ``rows`` int32 [M * k] (the flat token * k + slot of each row) and
+    ``pos`` int32 [M, k] (the row of each slot, -1 where it was dropped)."""
+
+    __slots__ = ("Xq", "s_x", "offsets", "rows", "pos")
+
+    def __init__(self, Xq, s_x, offsets, rows, pos):
+        self.Xq, self.s_x, self.offsets, self.rows, self.pos = Xq, s_x, offsets, rows, pos
+
+
+def w4a8_moe_dispatch(X, ids, experts, out=None, stream=None, flags=0):
+    """Group tokens X [M, K] (fp32 or bf16) by their experts ids int32 [M, k]
+    and quantize them into that order: a MoEDispatch (``out``, if given, is
+    filled; its rows behind the last expert's are left as they were).  Ids
+    outside [0, experts) drop their slot."""
+    kind = _typed(X, 2, "X")
+    _need(ids, _torch.int32, 2, "ids")
+    M, K = X.shape
+    k, E = ids.shape[1], int(experts)
+    if ids.shape[0] != M or k < 1 or E < 1:
+        raise ValueError("X has %d tokens, ids is %s, experts %d" % (M, tuple(ids.shape), E))
+    st = _together(stream, X, ids)
+    if out is None:
+        d = X.device
+        out = MoEDispatch(_new(stream, (M * k, K), _torch.int8, d),
+                          _new(stream, (M * k,), _torch.float32, d),
+                          _new(stream, (E + 1,), _torch.int32, d),
+                          _new(stream, (M * k,), _torch.int32, d),
+                          _new(stream, (M, k), _torch.int32, d))
+    else:
+        _out(out.Xq, _torch.int8, (M * k, K), X, "out.Xq")
+        _out(out.s_x, _torch.float32, (M * k,), X, "out.s_x")
+        _out(out.offsets, _torch.int32, (E + 1,), X, "out.offsets")
+        _out(out.rows, _torch.int32, (M * k,), X, "out.rows")
+        _out(out.pos, _torch.int32, (M, k), X, "out.pos")
+    _check(lib().w4a8_moe_dispatch(_ptr(X), kind, M, K, _ptr(ids), k, E, _ptr(out.Xq),
+                                   _ptr(out.s_x), _ptr(out.offsets), _ptr(out.rows),
+                                   _ptr(out.pos), int(flags), st), "w4a8_moe_dispatch")
+    return out
+
+
+def w4a8_moe_combine(Y, pos, weights, out=None, dtype=_torch.bfloat16, stream=None, flags=0):
+    """Bring expert outputs Y bf16 [R, N] back to tokens: out[m] (``dtype``
+    fp32 or bf16) = sum_j weights[m, j] * Y[pos[m, j]], pos outside [0, R)
+    adding nothing."""
+    _need(Y, _torch.bfloat16, 2, "Y")
+    _need(pos, _torch.int32, 2, "pos")
+    _need(weights, _torch.float32, 2, "weights")
+    if pos.shape != weights.shape:
+        raise ValueError("pos is %s, weights %s" % (tuple(pos.shape), tuple(weights.shape)))
+    (R, N), (M, k) = Y.shape, pos.shape
+    st = _together(stream, Y, pos, weights)
+    if out is None:
+        if dtype not in _TYPES:
+            raise TypeError("dtype must be float32 or bfloat16")
+        out = _new(stream, (M, N), dtype, Y.device)
+    else:
+        _typed(out, 2, "out")
+        _out(out, out.dtype, (M, N), Y, "out")
+    _check(lib().w4a8_moe_combine(_ptr(Y), R, N, _ptr(pos), _ptr(weights), M, k, _ptr(out),
+                                  _TYPES[out.dtype], int(flags), st), "w4a8_moe_combine")
+    return out
+
+
+class LoraPlan:
+    """Rows grouped by adapter (w4a8_lora_plan): ``offsets`` int32 [adapters +
+    1] and ``rows`` int32 [M].  It depends on the ids alone and is only read
+    by w4a8_lora, so one plan serves every layer of a step."""
+
+    __slots__ = ("offsets", "rows", "M", "adapters")
+
+    def __init__(self, offsets, rows, M, adapters):
+        self.offsets, self.rows, self.M, self.adapters = offsets, rows, M, adapters
+
+
+def w4a8_lora_plan(ids, adapters, out=None, stream=None, flags=0):
+    """The LoraPlan of ids int32 [M] (the adapter of each row; outside [0,
+    adapters): none), written into the plan ``out`` if given."""
+    _need(ids, _torch.int32, 1, "ids")
+    M, L = ids.numel(), int(adapters)
+    if L < 1:
+        raise ValueError("adapters must be positive")
+    st = _together(stream, ids)
+    if out is None:
+        out = LoraPlan(_new(stream, (L + 1,), _torch.int32, ids.device),
+                       _new(stream, (M,), _torch.int32, ids.device), M, L)
+    else:
+        if out.M != M or out.adapters != L:
+            raise ValueError("the plan is for %d rows and %d adapters" % (out.M, out.adapters))
+        _out(out.offsets, _torch.int32, (L + 1,), ids, "out.offsets")
+        _out(out.rows, _torch.int32, (M,), ids, "out.rows")
+    _check(lib().w4a8_lora_plan(_ptr(ids), M, L, _ptr(out.offsets), _ptr(out.rows), int(flags),
+                                st), "w4a8_lora_plan")
+    return out
+
+
+def w4a8_lora(X, Y, A, B, ids, scale=None, stream=None, flags=0):
+    """Add each row's low-rank adapter to the output of a shared projection, in
+    place: Y[m] += scale[a] * B[a] (A[a] x_m), a = ids[m]; rows whose id is
+    outside [0, L) are not touched.
+
+    X [M, K] fp32 or bf16 (the projection's input) and Y bf16 [M, N] (its
+    output) may have any row stride; A bf16 [L, r, K], B bf16 [L, N, r], scale
+    fp32 [L] or None.  ``ids`` is the int32 [M] tensor of adapters, or the
+    LoraPlan made of it (one plan serves every layer of a step; it is made
+    here where there are more than LORA_IDS_MAX rows and none is given).
+    Returns Y."""
+    for t, name in ((X, "X"), (Y, "Y")):
+        if not isinstance(t, _torch.Tensor) or not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise TypeError("%s must be 2D with adjacent columns" % name)
+    kind = _TYPES.get(X.dtype)
+    if kind is None or Y.dtype != _torch.bfloat16:
+        raise TypeError("X must be float32 or bfloat16 and Y bfloat16")
+    _need(A, _torch.bfloat16, 3, "A")
+    _need(B, _torch.bfloat16, 3, "B")
+    M, K = X.shape
+    N = Y.shape[1]
+    L, r = A.shape[:2]
+    if Y.shape[0] != M or A.shape[2] != K or tuple(B.shape) != (L, N, r):
+        raise ValueError("shape mismatch: X %s, Y %s, A %s, B %s" % (
+            tuple(X.shape), tuple(Y.shape), tuple(A.shape), tuple(B.shape)))
+    if scale is not None:
+        _need(scale, _torch.float32, 1, "scale")
+        if scale.numel() != L:
+            raise ValueError("scale has %d entries for %d adapters" % (scale.numel(), L))
+    plan = None
+    if isinstance(ids, LoraPlan):
+        plan, ids = ids, None
+        if plan.M != M or plan.adapters != L:
+            raise ValueError("the plan is for %d rows and %d adapters, not %d and %d"
+                             % (plan.M, plan.adapters, M, L))
+        st = _together(stream, X, Y, A, B, scale, plan.rows, plan.offsets)
+    else:
+        _need(ids, _torch.int32, 1, "ids")
+        if ids.numel() != M:
+            raise ValueError("%d ids for %d rows" % (ids.numel(), M))
+        st = _together(stream, X, Y, A, B, scale, ids)
+        if M > LORA_IDS_MAX:
+            # (the second kernel may start early: it waits before it reads)
+            plan, ids = w4a8_lora_plan(ids, L, stream=stream, flags=flags), None
+            flags = int(flags) | W4A8_FLAG_PDL
+    ldx = X.stride(0) if M > 1 else max(X.stride(0), K)
+    ldy = Y.stride(0) if M > 1 else max(Y.stride(0), N)
+    _check(lib().w4a8_lora(_ptr(X), kind, ldx, M, K, _ptr(A), _ptr(B), r, L, _ptr(scale),
+                           _ptr(ids), _ptr(plan.offsets) if plan else None,
+                           _ptr(plan.rows) if plan else None, N, _ptr(Y), ldy, int(flags), st),
+           "w4a8_lora")
     return Y
 
 

@@ -17,6 +17,8 @@
 #include "gemm_pp.cuh"
 #include "gemv.cuh"
 #include "layout.cuh"
+#include "lora.cuh"
+#include "moe.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 #include "w4a8.h"
@@ -908,6 +910,112 @@ int gemm_fused(const float* X, const void* packed, int M, int N, int K, uint16_t
   return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA;
 }
 
+// ------------------------------------- mixture-of-experts token side, adapters
+// Largest dynamic shared memory of a kernel, set once per device.
+template <typename F>
+cudaError_t ensure_smem(F* kernel, size_t bytes, std::atomic<bool>* done) {
+  const int dev = current_device();
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_relaxed))
+    return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices)
+    done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+bool is_type(int t) { return t == W4A8_TYPE_F32 || t == W4A8_TYPE_BF16; }
+int type_bytes(int t) { return t == W4A8_TYPE_F32 ? 4 : 2; }
+
+template <int NV>
+cudaError_t launch_route_nv(const RouteParams& p, int mode, cudaStream_t st, bool pdl) {
+  const dim3 grid((p.M + kRouteWarps - 1) / kRouteWarps), block(kRouteWarps * 32);
+  if (mode == 0) return launch_k(route_kernel<NV, 0>, grid, block, 0, st, pdl, 1, p);
+  if (mode == 1) return launch_k(route_kernel<NV, 1>, grid, block, 0, st, pdl, 1, p);
+  return launch_k(route_kernel<NV, 2>, grid, block, 0, st, pdl, 1, p);
+}
+
+cudaError_t launch_route(const RouteParams& p, int mode, cudaStream_t st, bool pdl) {
+  const int nv = (p.E / p.groups + p.lanes_per_group - 1) / p.lanes_per_group;
+  if (nv <= 1) return launch_route_nv<1>(p, mode, st, pdl);
+  if (nv <= 2) return launch_route_nv<2>(p, mode, st, pdl);
+  if (nv <= 4) return launch_route_nv<4>(p, mode, st, pdl);
+  if (nv <= 8) return launch_route_nv<8>(p, mode, st, pdl);
+  if (nv <= 16) return launch_route_nv<16>(p, mode, st, pdl);
+  return launch_route_nv<32>(p, mode, st, pdl);
+}
+
+// One CTA groups up to kGroupOneCta ids; more take a cluster.
+constexpr int kGroupOneCta = 4096;
+
+cudaError_t launch_group_rows(const int* ids, int n, int groups, int* offsets, int* rows, int* pos,
+                              cudaStream_t st, bool pdl) {
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = ensure_smem(group_rows_kernel, group_rows_smem(kMaxGroups), done);
+  if (e != cudaSuccess) return e;
+  const int ctas = n > kGroupOneCta ? kGroupCluster : 1;
+  return launch_k(group_rows_kernel, dim3(ctas), dim3(kGroupThreads), group_rows_smem(groups), st,
+                  pdl, ctas, ids, n, groups, ctas, offsets, rows, pos);
+}
+
+template <bool BF16, bool SMALL>
+cudaError_t launch_dispatch(const void* X, int M, int K, const int* ids, int top_k, int groups,
+                            int8_t* Xq, float* s_x, int* offsets, int* rows, int* pos,
+                            cudaStream_t st, bool pdl) {
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = ensure_smem(dispatch_kernel<BF16, SMALL>, 65536, done);
+  if (e != cudaSuccess) return e;
+  return launch_k(dispatch_kernel<BF16, SMALL>, dim3(SMALL ? M + 1 : M), dim3(kDispatchThreads),
+                  (size_t)K, st, pdl, 1, X, M, K, ids, top_k, groups, Xq, s_x, offsets, rows, pos);
+}
+
+template <typename OutT, int VEC>
+cudaError_t launch_combine(const uint16_t* Y, int rows, int N, const int* pos,
+                           const float* weights, int M, int top_k, OutT* out, cudaStream_t st,
+                           bool pdl) {
+  const int per = kCombineThreads * VEC;
+  return launch_k(combine_kernel<OutT, VEC>, dim3(M, (N + per - 1) / per), dim3(kCombineThreads),
+                  0, st, pdl, 1, Y, rows, N, pos, weights, top_k, out);
+}
+
+template <bool BF16X, int NT, int WR>
+cudaError_t launch_lora_as(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
+  static std::atomic<bool> done[kMaxDevices];
+  constexpr int smem = LoraCfg<NT, WR>::kSmemBytes;
+  const cudaError_t e = ensure_smem(lora_kernel<BF16X, NT, WR>, smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_k(lora_kernel<BF16X, NT, WR>, dim3(slots * p.ctas, parts), dim3(kLoraThreads), smem,
+                  st, pdl, p.ctas, p);
+}
+
+template <bool BF16X, int WR>
+cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
+  if (p.rank <= 16) return launch_lora_as<BF16X, 2, WR>(p, slots, parts, st, pdl);
+  if (p.rank <= 32) return launch_lora_as<BF16X, 4, WR>(p, slots, parts, st, pdl);
+  if (p.rank <= 64) return launch_lora_as<BF16X, 8, WR>(p, slots, parts, st, pdl);
+  return launch_lora_as<BF16X, 16, WR>(p, slots, parts, st, pdl);
+}
+
+// Row tiles of 64 where adapters have that many rows on average, else of 16;
+// a tile's cluster and the further split of N grow until the CTAs cover the
+// machine twice, while a CTA keeps a k step per warp and 8 column slices.
+cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool pdl) {
+  const int used = p.adapters < p.M ? p.adapters : p.M;
+  const bool tall = p.M / used >= 32;
+  const int tm = tall ? 64 : 16;
+  const int slots = (int)(((long long)p.M + (long long)used * (tm - 1)) / tm);
+  const int wk = tall ? kLoraWarps / 4 : kLoraWarps;
+  int ctas = 1, parts = 1;
+  while (ctas < 8 && (long long)slots * ctas < 2 * sms && p.K / 32 >= 2 * ctas * wk) ctas *= 2;
+  while ((long long)slots * ctas * parts < 2 * sms && p.N / 32 >= 2 * ctas * parts * 8) parts *= 2;
+  p.ctas = ctas;
+  if (tall)
+    return bf16x ? launch_lora_nt<true, 4>(p, slots, parts, st, pdl)
+                 : launch_lora_nt<false, 4>(p, slots, parts, st, pdl);
+  return bf16x ? launch_lora_nt<true, 1>(p, slots, parts, st, pdl)
+               : launch_lora_nt<false, 1>(p, slots, parts, st, pdl);
+}
+
 __global__ void timeout_probe_kernel(unsigned long long limit_ns) {
   __shared__ alignas(8) uint64_t bar;
   if (threadIdx.x == 0) {
@@ -1132,6 +1240,168 @@ int w8a8_gemm_schedule(int M, int N, int K, int* tile_tokens, int* splits, int* 
   if (splits) *splits = s.splits;
   if (ctas) *ctas = s.ctas;
   return W4A8_OK;
+}
+
+int w4a8_moe_route(const void* logits, int logits_type, int M, int E, int top_k, int score,
+                   const float* bias, int groups, int top_groups, int group_top, int renormalize,
+                   float scale, int32_t* ids, float* weights, unsigned flags, void* stream) {
+  if (flags & ~(unsigned)W4A8_FLAG_PDL) return W4A8_ERR_INVALID_ARG;
+  if (!is_type(logits_type) || M < 0 || E < 1 || top_k < 1 || groups < 1)
+    return W4A8_ERR_INVALID_ARG;
+  if (score != W4A8_SCORE_SOFTMAX && score != W4A8_SCORE_SIGMOID) return W4A8_ERR_INVALID_ARG;
+  if (group_top != 1 && group_top != 2) return W4A8_ERR_INVALID_ARG;
+  if (E % groups != 0 || top_groups < 1 || top_groups > groups) return W4A8_ERR_INVALID_ARG;
+  if (top_k > (long long)top_groups * (E / groups)) return W4A8_ERR_INVALID_ARG;
+  int lanes = 32;
+  while (lanes > 0 && 32 / lanes < groups) lanes /= 2;
+  if (top_k > kMaxTopK || lanes == 0 || E / groups > 32 * lanes) return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return W4A8_OK;
+  if (!logits || !ids || !weights) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(logits, type_bytes(logits_type)) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(bias, 4))
+    return W4A8_ERR_MISALIGNED;
+  RouteParams p;
+  p.logits = logits;
+  p.bf16 = logits_type == W4A8_TYPE_BF16;
+  p.M = M;
+  p.E = E;
+  p.k = top_k;
+  p.sigmoid = score == W4A8_SCORE_SIGMOID;
+  p.bias = bias;
+  p.groups = groups;
+  p.top_groups = top_groups;
+  p.group_top = group_top;
+  p.lanes_per_group = lanes;
+  p.renormalize = renormalize != 0;
+  p.scale = scale;
+  p.ids = ids;
+  p.weights = weights;
+  const int mode = bias ? 2 : (groups > 1 && group_top == 2 ? 1 : 0);
+  return launch_route(p, mode, as_stream(stream), (flags & W4A8_FLAG_PDL) != 0) == cudaSuccess
+             ? W4A8_OK
+             : W4A8_ERR_CUDA;
+}
+
+int w4a8_moe_dispatch(const void* X, int x_type, int M, int K, const int32_t* ids, int top_k,
+                      int experts, int8_t* Xq, float* s_x, int32_t* offsets, int32_t* rows,
+                      int32_t* pos, unsigned flags, void* stream) {
+  if (flags & ~(unsigned)W4A8_FLAG_PDL) return W4A8_ERR_INVALID_ARG;
+  if (!is_type(x_type) || M < 0 || K < 1 || top_k < 1 || experts < 1 || !offsets)
+    return W4A8_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > 65536 || top_k > kMaxTopK || experts > kMaxGroups ||
+      (long long)M * top_k > (1 << 30))
+    return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (M > 0 && (!X || !ids || !Xq || !s_x || !rows || !pos)) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || !aligned(Xq, 16) || !aligned(ids, 4) || !aligned(s_x, 4) ||
+      !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(pos, 4))
+    return W4A8_ERR_MISALIGNED;
+  const bool pdl = (flags & W4A8_FLAG_PDL) != 0;
+  const bool bf16 = x_type == W4A8_TYPE_BF16;
+  cudaStream_t st = as_stream(stream);
+  cudaError_t e;
+  if (M > 0 && M * (long long)top_k <= kDispatchSmall) {
+    e = bf16 ? launch_dispatch<true, true>(X, M, K, ids, top_k, experts, Xq, s_x, offsets, rows,
+                                           pos, st, pdl)
+             : launch_dispatch<false, true>(X, M, K, ids, top_k, experts, Xq, s_x, offsets, rows,
+                                            pos, st, pdl);
+    return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA;
+  }
+  e = launch_group_rows(ids, M * top_k, experts, offsets, rows, pos, st, pdl);
+  if (e != cudaSuccess) return W4A8_ERR_CUDA;
+  if (M == 0) return W4A8_OK;
+  // (the second kernel may start early whatever the flags: it reads only X
+  // before it waits for the places, and the first kernel lets it start only
+  // once everything before it is done)
+  e = bf16 ? launch_dispatch<true, false>(X, M, K, ids, top_k, experts, Xq, s_x, offsets, rows, pos,
+                                          st, true)
+           : launch_dispatch<false, false>(X, M, K, ids, top_k, experts, Xq, s_x, offsets, rows,
+                                           pos, st, true);
+  return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA;
+}
+
+int w4a8_moe_combine(const uint16_t* Y, int rows, int N, const int32_t* pos, const float* weights,
+                     int M, int top_k, void* out, int out_type, unsigned flags, void* stream) {
+  if (flags & ~(unsigned)W4A8_FLAG_PDL) return W4A8_ERR_INVALID_ARG;
+  if (!is_type(out_type) || M < 0 || N < 1 || rows < 0 || top_k < 1) return W4A8_ERR_INVALID_ARG;
+  if (top_k > kMaxTopK || (N + kCombineThreads - 1) / kCombineThreads > 65535)
+    return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return W4A8_OK;
+  if ((rows > 0 && !Y) || !pos || !weights || !out) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(Y, 2) || !aligned(pos, 4) || !aligned(weights, 4) ||
+      !aligned(out, type_bytes(out_type)))
+    return W4A8_ERR_MISALIGNED;
+  const bool pdl = (flags & W4A8_FLAG_PDL) != 0;
+  const bool vec = N % 8 == 0 && aligned(Y, 16) && aligned(out, 16);
+  cudaStream_t st = as_stream(stream);
+  cudaError_t e;
+  if (out_type == W4A8_TYPE_F32) {
+    float* o = static_cast<float*>(out);
+    e = vec ? launch_combine<float, 8>(Y, rows, N, pos, weights, M, top_k, o, st, pdl)
+            : launch_combine<float, 1>(Y, rows, N, pos, weights, M, top_k, o, st, pdl);
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+    e = vec ? launch_combine<__nv_bfloat16, 8>(Y, rows, N, pos, weights, M, top_k, o, st, pdl)
+            : launch_combine<__nv_bfloat16, 1>(Y, rows, N, pos, weights, M, top_k, o, st, pdl);
+  }
+  return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA;
+}
+
+int w4a8_lora_plan(const int32_t* ids, int M, int adapters, int32_t* offsets, int32_t* rows,
+                   unsigned flags, void* stream) {
+  if (flags & ~(unsigned)W4A8_FLAG_PDL) return W4A8_ERR_INVALID_ARG;
+  if (M < 0 || adapters < 1 || !offsets) return W4A8_ERR_INVALID_ARG;
+  if (adapters > kLoraMaxAdapters || M > (1 << 30)) return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (M > 0 && (!ids || !rows)) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(rows, 4)) return W4A8_ERR_MISALIGNED;
+  return launch_group_rows(ids, M, adapters, offsets, rows, nullptr, as_stream(stream),
+                           (flags & W4A8_FLAG_PDL) != 0) == cudaSuccess
+             ? W4A8_OK
+             : W4A8_ERR_CUDA;
+}
+
+int w4a8_lora(const void* X, int x_type, long long ldx, int M, int K, const uint16_t* A,
+              const uint16_t* B, int rank, int adapters, const float* scale, const int32_t* ids,
+              const int32_t* offsets, const int32_t* rows, int N, uint16_t* Y, long long ldy,
+              unsigned flags, void* stream) {
+  if (flags & ~(unsigned)W4A8_FLAG_PDL) return W4A8_ERR_INVALID_ARG;
+  if (!is_type(x_type) || M < 0 || K < 1 || N < 1 || rank < 1 || adapters < 1)
+    return W4A8_ERR_INVALID_ARG;
+  if (K % kTileK != 0 || K > 65536 || rank % 8 != 0 || rank > kLoraMaxRank ||
+      adapters > kLoraMaxAdapters || M > (1 << 24))
+    return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (ids && M > kLoraIdsMax) return W4A8_ERR_UNSUPPORTED_SHAPE;
+  if (ldx < K || ldy < N) return W4A8_ERR_INVALID_ARG;
+  if (M == 0) return W4A8_OK;
+  if (!X || !A || !B || !Y) return W4A8_ERR_INVALID_ARG;
+  if (ids ? (offsets || rows) : (!offsets || !rows)) return W4A8_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || (ldx * type_bytes(x_type)) % 16 != 0 || !aligned(A, 16) ||
+      !aligned(B, 16) || !aligned(Y, 2) || !aligned(scale, 4) || !aligned(ids, 4) ||
+      !aligned(offsets, 4) || !aligned(rows, 4))
+    return W4A8_ERR_MISALIGNED;
+  const int dev = current_device();
+  if (dev < 0) return W4A8_ERR_CUDA;
+  LoraParams p;
+  p.X = X;
+  p.ldx = ldx;
+  p.M = M;
+  p.K = K;
+  p.N = N;
+  p.rank = rank;
+  p.adapters = adapters;
+  p.A = A;
+  p.B = B;
+  p.scale = scale;
+  p.ids = ids;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.Y = Y;
+  p.ldy = ldy;
+  p.y_vec = aligned(Y, 16) && ldy % 8 == 0;
+  p.ctas = 1;
+  return launch_lora(p, x_type == W4A8_TYPE_BF16, num_sms(dev), as_stream(stream),
+                     (flags & W4A8_FLAG_PDL) != 0) == cudaSuccess
+             ? W4A8_OK
+             : W4A8_ERR_CUDA;
 }
 
 int w4a8_get_status(void* stream) {

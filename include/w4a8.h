@@ -328,6 +328,121 @@ int w4a8_grouped_gemm_schedule(int groups, int M_total, int max_rows, int N,
                                int K, int* tile_tokens, int* splits, int* ctas);
 
 /*
+ * ---- The token side of a mixture-of-experts layer ----
+ * Router logits to experts, tokens to the rows that w4a8_grouped_gemm reads,
+ * and the experts' outputs back to tokens:
+ *   w4a8_moe_route -> w4a8_moe_dispatch -> w4a8_grouped_gemm (...) ->
+ *   w4a8_moe_combine
+ * All on the device: the offsets never visit the host.  W4A8_TYPE_* name the
+ * element type of arguments that may have more than one.
+ */
+#define W4A8_TYPE_F32 0
+#define W4A8_TYPE_BF16 1
+
+#define W4A8_SCORE_SOFTMAX 0
+#define W4A8_SCORE_SIGMOID 1
+
+/*
+ * Routing.  logits [M][E] (fp32 or bf16) -> ids [M][top_k] int32 and
+ * weights [M][top_k] fp32.
+ *   scores      p_e = softmax(logits)_e or sigmoid(logit_e)
+ *   order       by p_e, or by p_e + bias_e where bias [E] (fp32, finite) is
+ *               given; the bias takes no part in the weights
+ *   groups      the experts form `groups` runs of E / groups; a run's score is
+ *               its best expert's (group_top = 1) or the sum of its two
+ *               best (2), and only the top_groups best runs' experts are open
+ *   choice      the top_k best open experts, best first
+ *   weights     their p_e, with `renormalize` divided by their sum, times scale
+ * Ties go to the lowest index, of groups and of experts.  The order is that
+ * of the exact scores: of the logits without a bias, and of p_e + bias_e in
+ * fp64 with one; groups scored by two are compared in fp64 too.
+ * A logit of -inf, NaN, or at or below bf16's lowest finite value
+ * (-3.3895e38) is a mask: that expert is never chosen.  Where fewer than
+ * top_k experts are open the last ids are -1 with weight 0.  +inf logits
+ * share a softmax equally.
+ * top_k <= 32 and E / groups <= 32 * L, L = 32 / groups with groups rounded up
+ * to a power of two (so E <= 1024 and groups <= 32), else
+ * W4A8_ERR_UNSUPPORTED_SHAPE; top_k may not exceed the open experts.
+ * M == 0 is a no-op.  flags: W4A8_FLAG_PDL or 0, as everywhere below: the
+ * kernel may start early, and reads nothing but weights before the preceding
+ * kernel is done.
+ */
+int w4a8_moe_route(const void* logits, int logits_type, int M, int E, int top_k,
+                   int score, const float* bias, int groups, int top_groups,
+                   int group_top, int renormalize, float scale, int32_t* ids,
+                   float* weights, unsigned flags, void* stream);
+
+/*
+ * Dispatch: tokens X [M][K] (fp32 or bf16) to rows grouped by expert, and
+ * quantized by the rule of w4a8_quantize_act on the way.  ids [M][top_k]
+ * int32; the pair i = m * top_k + j is token m's slot j.
+ *   offsets [experts + 1]  the rows of expert e are offsets[e] ..
+ *                          offsets[e + 1] - 1, in the order of their pairs
+ *   pos [M][top_k]         the row of each pair; -1 for an id outside
+ *                          [0, experts) (a dropped slot)
+ *   rows [M * top_k]       the pair of each row
+ *   Xq [M * top_k][K] int8, s_x [M * top_k] fp32: the rows
+ * Rows at and behind offsets[experts] are left as they were, in rows, Xq and
+ * s_x alike.  offsets go to w4a8_grouped_gemm with M_total = M * top_k (rows
+ * behind its last offset are left alone there too).  No expert has more than
+ * M rows if a token's ids differ, so max_rows = M then.
+ * K a positive multiple of 16, K <= 65536, top_k <= 32, experts <= 1024,
+ * M * top_k <= 2^30.  X, Xq 16-byte aligned, else 4.  M == 0 writes offsets
+ * of zero.
+ */
+int w4a8_moe_dispatch(const void* X, int x_type, int M, int K,
+                      const int32_t* ids, int top_k, int experts, int8_t* Xq,
+                      float* s_x, int32_t* offsets, int32_t* rows,
+                      int32_t* pos, unsigned flags, void* stream);
+
+/*
+ * Combine: out[m] = sum_j weights[m][j] * Y[pos[m][j]], summed in fp32 in
+ * the order of j and rounded once.  Y [rows][N] bf16, pos and weights
+ * [M][top_k], out [M][N] fp32 or bf16.  A pos outside [0, rows) adds nothing
+ * (a token without any row gets zeros).  top_k <= 32.  Y and out need their
+ * elements' alignment; 16 bytes and N a multiple of 8 are faster.
+ */
+int w4a8_moe_combine(const uint16_t* Y, int rows, int N, const int32_t* pos,
+                     const float* weights, int M, int top_k, void* out,
+                     int out_type, unsigned flags, void* stream);
+
+/*
+ * ---- Low-rank adapters beside a shared projection ----
+ * For every row m whose adapter a = ids[m] is in [0, adapters):
+ *   Y[m] = bf16_rn( Y[m] + scale[a] * B[a] (A[a] x_m) )
+ * in place on the shared projection's output (w4a8_gemm), any mixture of
+ * adapters in one launch; other rows are not touched.
+ *   X [M] rows of K, fp32 or bf16, ldx elements apart; Y [M] rows of N bf16,
+ *   ldy elements apart (a column block of a wider matrix is fine);
+ *   A [adapters][rank][K], B [adapters][N][rank] bf16, scale [adapters] fp32
+ *   or NULL (all 1).
+ * Sums are fp32.  fp32 X and A x enter the products as two bf16 terms
+ * each (16 bits of them); the sum with Y is rounded once.  |X| < 3.38e38.
+ * The rows are given in one of two ways:
+ *   ids [M] int32, offsets = rows = NULL: for M <= 256;
+ *   ids = NULL, offsets and rows from w4a8_lora_plan for these ids.
+ * A plan depends on the ids alone, so one serves every layer of a step; it is
+ * only read, and any number of calls may share it.
+ * rank a multiple of 8, <= 128 (pad with zeros); adapters <= 1024; K as for
+ * w4a8_gemm; M <= 2^24.  X, A and B 16-byte aligned, ldx * its element size
+ * a multiple of 16, Y 2-byte aligned (16 with ldy a multiple of 8 is faster).
+ * Y may not overlap the other arguments.
+ */
+int w4a8_lora(const void* X, int x_type, long long ldx, int M, int K,
+              const uint16_t* A, const uint16_t* B, int rank, int adapters,
+              const float* scale, const int32_t* ids, const int32_t* offsets,
+              const int32_t* rows, int N, uint16_t* Y, long long ldy,
+              unsigned flags, void* stream);
+
+/*
+ * Groups rows by adapter: offsets [adapters + 1], rows [M] int32 (device);
+ * adapter a has rows[offsets[a]] .. rows[offsets[a + 1] - 1], in increasing
+ * order.  Entries of rows behind offsets[adapters] are left as they were.
+ */
+int w4a8_lora_plan(const int32_t* ids, int M, int adapters, int32_t* offsets,
+                   int32_t* rows, unsigned flags, void* stream);
+
+/*
  * ---- W8A8 comparison point ----
  * The review page (pith summary; forward implication 3) measures the method
  * against W8A8: 8-bit weights that need no dequantization.  These entry

@@ -1,0 +1,219 @@
+"""The low-rank adapters on the GPU against their 64-bit statement, beside the
+projection they belong to."""
+import numpy as np
+import pytest
+import torch
+
+import bit_block_quantized_w4a8_b200 as w4
+import moe_plain as plain
+from bit_block_quantized_w4a8_b200 import workloads as wl
+from gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+    torch.cuda.set_device(0)
+    assert w4.w4a8_get_status() == 0
+    yield
+    assert w4.w4a8_get_status() == 0
+
+
+def _weights(L, K, N, r, seed):
+    A = wl.random_matrix(L * r, K, seed, std=K ** -0.5).view(L, r, K).bfloat16().cuda()
+    B = wl.random_matrix(L * N, r, seed + 1, std=0.5 * r ** -0.5).view(L, N, r).bfloat16().cuda()
+    scale = (torch.rand(L, generator=torch.Generator().manual_seed(seed)) * 2 - 0.5).cuda()
+    return A, B, scale
+
+
+def _ids(M, L, seed, runs):
+    r = np.random.RandomState(seed)
+    if runs:
+        ids = r.randint(-1, L, M)[np.sort(r.randint(0, max(1, M // 20), M))]
+    else:
+        ids = r.randint(-1, L + 1, M)   # L: outside as well
+    return ids.astype(np.int32)
+
+
+def check(Y0, Y1, X, A, B, ids, scale):
+    """Y1, the result, against Y0 + the adapters; untouched rows bit for bit."""
+    f = lambda t: None if t is None else t.double().cpu().numpy()
+    ref, tol = plain.lora(f(X), f(Y0), f(A), f(B), ids, f(scale))
+    tol += 2.0 ** -8 * (np.abs(ref) + tol)   # half a bf16 step of the sum
+    assert np.all(np.abs(f(Y1) - ref) <= tol)
+    none = (ids < 0) | (ids >= A.shape[0])
+    none = torch.from_numpy(none).cuda()
+    assert torch.equal(Y1[none].view(torch.int16), Y0[none].view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K,N,r,L,runs", [
+    (1, 128, 1, 8, 1, False), (1, 4096, 4096, 16, 4, False), (2, 256, 33, 24, 3, False),
+    (5, 384, 200, 40, 7, False), (16, 1024, 96, 64, 2, False), (17, 512, 70, 128, 1, False),
+    (64, 2048, 512, 16, 64, False), (255, 640, 264, 32, 5, False), (256, 256, 128, 104, 9, True),
+    (256, 256, 72, 8, 1, False),
+    # planned
+    (257, 256, 136, 16, 4, False), (400, 1152, 301, 64, 3, True), (1000, 128, 64, 128, 2, True),
+    (700, 384, 96, 24, 300, False), (300, 256, 64, 8, 1024, False), (5000, 256, 40, 32, 12, True)])
+def test_lora(M, K, N, r, L, runs, dtype):
+    A, B, scale = _weights(L, K, N, r, 10 * M + r)
+    X = wl.random_matrix(M, K, M + K, kind="heavy").to(dtype).cuda()
+    Y0 = wl.random_matrix(M, N, M + N).bfloat16().cuda()
+    ids = _ids(M, L, M, runs)
+    d = torch.from_numpy(ids).cuda()
+    Y = Y0.clone()
+    assert w4.w4a8_lora(X, Y, A, B, d, scale=scale) is Y
+    check(Y0, Y, X, A, B, ids, scale)
+    # the same through a plan, without a scale
+    plan = w4.w4a8_lora_plan(d, L)
+    Y2 = Y0.clone()
+    w4.w4a8_lora(X, Y2, A, B, plan)
+    check(Y0, Y2, X, A, B, ids, None)
+
+
+def test_lora_plan():
+    for M, L in ((0, 3), (1, 1), (300, 5), (5000, 1000), (20011, 64)):
+        ids = _ids(M, L, M + 1, False)
+        p = w4.w4a8_lora_plan(torch.from_numpy(ids).cuda(), L)
+        offsets, rows, _ = plain.places(ids, L)
+        assert np.array_equal(p.offsets.cpu().numpy(), offsets)
+        assert np.array_equal(p.rows.cpu().numpy()[:len(rows)], rows)
+        again = w4.w4a8_lora_plan(torch.from_numpy(ids).cuda(), L, out=p)
+        assert again is p
+
+
+def test_lora_strides_and_neighbours():
+    """Column blocks of wider matrices: what lies beside them stays as it was,
+    for aligned and odd positions."""
+    M, K, r, L = 40, 256, 16, 3
+    ids = _ids(M, L, 4, False)
+    d = torch.from_numpy(ids).cuda()
+    wide = wl.random_matrix(M, 2 * K + 64, 5).cuda()
+    for dtype in (torch.float32, torch.bfloat16):
+        for y0, N, ld in ((0, 64, 64), (8, 64, 128), (3, 61, 99), (16, 40, 1000), (1, 1, 7)):
+            A, B, scale = _weights(L, K, N, r, 6 + N)
+            X = wide.to(dtype)[:, 32:32 + K]
+            big = wl.random_matrix(M, ld, 7).bfloat16().cuda()
+            before = big.clone()
+            w4.w4a8_lora(X, big[:, y0:y0 + N], A, B, d, scale=scale)
+            check(before[:, y0:y0 + N], big[:, y0:y0 + N], X, A, B, ids, scale)
+            big[:, y0:y0 + N] = before[:, y0:y0 + N]
+            assert torch.equal(big.view(torch.int16), before.view(torch.int16))
+
+
+def test_lora_no_rows_and_no_adapter():
+    A, B, scale = _weights(3, 128, 64, 8, 1)
+    X = wl.random_matrix(6, 128, 2).cuda()
+    Y0 = wl.random_matrix(6, 64, 3).bfloat16().cuda()
+    for ids in ([-1] * 6, [3, 4, -7, 1 << 30, -1, 3]):
+        d = torch.tensor(ids, dtype=torch.int32, device="cuda")
+        Y = Y0.clone()
+        w4.w4a8_lora(X, Y, A, B, d, scale=scale)
+        w4.w4a8_lora(X, Y, A, B, w4.w4a8_lora_plan(d, 3), scale=scale)
+        assert torch.equal(Y.view(torch.int16), Y0.view(torch.int16))
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert w4.w4a8_lora(X[:0], Y0[:0], A, B, e).shape == (0, 64)
+    assert w4.w4a8_lora(X[:0], Y0[:0], A, B, w4.w4a8_lora_plan(e, 3)).shape == (0, 64)
+
+
+def test_lora_precision_is_above_one_bf16_term():
+    """fp32 activations keep 16 bits: against a result whose rounding is seen
+    (zero base, single rank), far below one bf16 rounding of x."""
+    K, N = 4096, 64
+    X = wl.random_matrix(32, K, 21).cuda()
+    A = torch.ones(1, 8, K, device="cuda").bfloat16()
+    B = torch.zeros(1, N, 8, device="cuda").bfloat16()
+    B[0, :, 0] = 1.0
+    Y = torch.zeros(32, N, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(32, dtype=torch.int32, device="cuda")
+    w4.w4a8_lora(X, Y, A, B, ids)
+    t = X.double().sum(1, keepdim=True).cpu().numpy()
+    mag = X.double().abs().sum(1, keepdim=True).cpu().numpy()
+    err = np.abs(Y.double().cpu().numpy() - t)
+    assert np.all(err <= 2.0 ** -8 * np.abs(t) + (2.0 ** -16 + (K / 8 + 32) * 2.0 ** -22) * mag)
+
+
+def test_lora_is_deterministic_and_a_plan_is_shared():
+    """Two layers with one plan on two streams at once, and twice: the same
+    bits as one after the other."""
+    M, K, N, r, L = 600, 512, 512, 32, 7
+    ids = torch.from_numpy(_ids(M, L, 8, True)).cuda()
+    plan = w4.w4a8_lora_plan(ids, L)
+    layers = [_weights(L, K, N, r, 30 + i) for i in range(2)]
+    X = wl.random_matrix(M, K, 31).cuda()
+    Y0 = wl.random_matrix(M, N, 32).bfloat16().cuda()
+    want = [w4.w4a8_lora(X, Y0.clone(), A, B, plan, scale=s) for A, B, s in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    got = [Y0.clone() for _ in layers]
+    torch.cuda.synchronize()
+    for Y, st, (A, B, s) in zip(got, streams, layers):
+        w4.w4a8_lora(X, Y, A, B, plan, scale=s, stream=st)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("M", [3, 200, 900])
+@pytest.mark.parametrize("flags", [0, w4.W4A8_FLAG_PDL])
+def test_lora_beside_the_projection_captured_and_replayed(M, flags):
+    """Quantize, W4A8 GEMM, adapters: captured, replayed for other requests'
+    ids and inputs, against the GEMM's own output plus the adapters."""
+    K, N, r, L = 512, 384, 16, 6
+    W = wl.random_matrix(N, K, 40, std=0.02).cuda()
+    pk = w4.w4a8_quantize_weights(W)
+    A, B, scale = _weights(L, K, N, r, 41)
+    X = torch.empty(M, K, device="cuda")
+    ids = torch.empty(M, dtype=torch.int32, device="cuda")
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    cases = [(wl.random_matrix(M, K, 42 + i).cuda(), _ids(M, L, 43 + i, i == 1)) for i in range(3)]
+    X.copy_(cases[0][0])
+    ids.copy_(torch.from_numpy(cases[0][1]))
+
+    def step():
+        Xq, sx = w4.w4a8_quantize_act(X, flags=flags)
+        w4.w4a8_gemm(Xq, sx, pk, out=Y, flags=flags)
+        w4.w4a8_lora(X, Y, A, B, ids, scale=scale, flags=flags)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for x, i in cases:
+        X.copy_(x)
+        ids.copy_(torch.from_numpy(i))
+        graph.replay()
+        base = w4.w4a8_gemm(*w4.w4a8_quantize_act(x), pk)
+        check(base, Y, x, A, B, i, scale)
+    assert w4.w4a8_get_status() == 0
+    del graph
+
+
+def test_lora_refusals():
+    A, B, scale = _weights(2, 128, 16, 8, 50)
+    X = torch.zeros(4, 128, device="cuda")
+    Y = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros(4, dtype=torch.int32, device="cuda")
+    plan = w4.w4a8_lora_plan(ids, 2)
+    for a, err in (((X.half(), Y, A, B, ids), TypeError), ((X, Y.float(), A, B, ids), TypeError),
+                   ((X, Y, A.float(), B, ids), TypeError), ((X, Y, A, B, ids.long()), TypeError),
+                   ((X, Y, A, B, ids[:3]), ValueError), ((X[:3], Y, A, B, ids), ValueError),
+                   ((X, Y, A, B[:1], ids), ValueError), ((X, Y, A, B.cpu(), ids), TypeError),
+                   ((X[:3], Y[:3], A, B, plan), ValueError),
+                   ((X, Y, A[:1], B[:1], plan), ValueError),
+                   ((X[:, :64], Y, A, B, ids), ValueError),
+                   ((X, Y.t().contiguous().t(), A, B, ids), TypeError),
+                   ((X[:1].expand(4, 128), Y, A, B, ids), w4.W4A8Error),
+                   ((X, Y[:1].expand(4, 16), A, B, ids), w4.W4A8Error)):
+        with pytest.raises(err):
+            w4.w4a8_lora(*a)
+    with pytest.raises(ValueError):
+        w4.w4a8_lora(X, Y, A, B, ids, scale=scale[:1])
+    with pytest.raises(w4.W4A8Error):
+        w4.w4a8_lora(X, Y, A[:, :4].contiguous(), B[:, :, :4].contiguous(), ids)
+    with pytest.raises(ValueError):
+        w4.w4a8_lora_plan(ids, 3, out=plan)
+    torch.cuda.synchronize()
+    assert not Y.any()

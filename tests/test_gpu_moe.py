@@ -1,0 +1,370 @@
+"""The mixture-of-experts token operators on the GPU against their 64-bit
+statements: routing (ids equal, weights to fp32), dispatch (places equal,
+codes and scales bit-exact against the quantizer's oracle), combine, and the
+whole layer around the grouped GEMM."""
+import numpy as np
+import pytest
+import torch
+
+import bit_block_quantized_w4a8_b200 as w4
+import moe_plain as plain
+import oracle
+from bit_block_quantized_w4a8_b200 import workloads as wl
+from gpu_util import assert_bf16_within_1ulp, bf16_bits, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+    torch.cuda.set_device(0)
+    assert w4.w4a8_get_status() == 0
+    yield
+    assert w4.w4a8_get_status() == 0
+
+
+# ---------------------------------------------------------------- routing
+# Relative error of a weight: the exponent's difference is rounded (2^-24 of
+# at most 40 here), two exponentials (2 ulp each at most), a sum of positive
+# terms (32 in a lane at most, 5 steps over lanes), a division and a product:
+# under 2^-24 * (40 + 8 + 37 + 4) < 2^-17.
+W_TOL = 2.0 ** -17
+
+
+def check_route(logits, k, **kw):
+    bias = kw.get("bias")
+    ids, w = w4.w4a8_moe_route(logits, k, **kw)
+    kw = dict(kw, bias=None if bias is None else bias.cpu().numpy())
+    ref_ids, ref_w = plain.route(logits.float().cpu().numpy(), k, **kw)
+    ids, w = ids.cpu().numpy(), w.cpu().numpy().astype(np.float64)
+    assert np.array_equal(ids, ref_ids)
+    assert np.all(np.abs(w - ref_w) <= W_TOL * np.abs(ref_w) + 1e-37)
+
+
+def _logits(M, E, seed, dtype=torch.float32, std=2.0):
+    return wl.random_matrix(M, E, seed, std=std).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("M,E,k", [(1, 8, 2), (3, 1, 1), (5, 2, 2), (7, 31, 4), (33, 33, 5),
+                                   (9, 60, 6), (130, 128, 8), (6, 257, 32), (4, 513, 10),
+                                   (5, 1024, 9)])
+def test_route(M, E, k, score, dtype):
+    l = _logits(M, E, 100 + E, dtype)
+    check_route(l, k, score=score)
+    check_route(l, k, score=score, renormalize=False, scale=2.5)
+    # (a bias apart for every expert: equal bf16 logits do not tie then)
+    bias = wl.random_matrix(1, E, 200 + E, std=0.3)[0].cuda()
+    check_route(l, k, score=score, bias=bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("M,E,k,groups,top_groups", [
+    (3, 8, 2, 2, 1), (17, 256, 8, 8, 4), (5, 160, 6, 8, 3), (4, 35, 7, 5, 2), (6, 32, 3, 32, 3),
+    (6, 64, 6, 32, 3), (2, 1024, 8, 32, 4), (2, 640, 8, 5, 1), (9, 12, 12, 3, 3)])
+def test_route_groups(M, E, k, groups, top_groups, group_top, score):
+    l = _logits(M, E, 300 + E + groups)
+    kw = dict(score=score, groups=groups, top_groups=top_groups, group_top=group_top)
+    check_route(l, k, **kw)
+    check_route(l, k, bias=wl.random_matrix(1, E, 301, std=0.5)[0].cuda(), renormalize=False, **kw)
+
+
+def test_route_ties_go_to_the_lowest_index():
+    l = torch.zeros(4, 100, device="cuda")
+    l[1, ::2] = 1.0
+    l[2] = -0.0
+    l[2, 50:] = 0.0   # the two zeros are one value
+    l[3, 10] = l[3, 90] = 3.0
+    check_route(l, 7)
+    check_route(l, 7, score="sigmoid")
+    check_route(l, 7, bias=torch.zeros(100, device="cuda"))
+    for top in (1, 2):
+        check_route(l, 7, groups=10, top_groups=3, group_top=top)
+        check_route(l, 7, groups=10, top_groups=3, group_top=top, score="sigmoid",
+                    bias=torch.full((100,), 0.25, device="cuda"))
+    # few distinct values, as bf16 logits have
+    q = (torch.randn(64, 128, generator=torch.Generator().manual_seed(5)) * 2).round().cuda()
+    check_route(q, 8)
+    check_route(q.bfloat16(), 8, score="sigmoid", bias=torch.zeros(128, device="cuda"))
+    check_route(q, 8, groups=8, top_groups=4, group_top=2)
+
+
+def test_route_borders_closer_than_fp32():
+    """Scores that fp32 cannot tell apart are told apart: saturated sigmoids,
+    and a bias that reverses two scores by less than an fp32 step."""
+    l = torch.tensor([[20.0, 30.0, 25.0, 10.0], [-60.0, -50.0, -70.0, -80.0]], device="cuda")
+    check_route(l, 3, score="sigmoid")
+    check_route(l, 3, score="sigmoid", bias=torch.zeros(4, device="cuda"))
+    l = torch.tensor([[2.0, 2.0 + 2 ** -22, 1.0]], device="cuda")
+    for b in (2.0 ** -27, 2.0 ** -25, -(2.0 ** -26)):
+        check_route(l, 2, score="sigmoid", bias=torch.tensor([b, 0.0, 0.0], device="cuda"))
+        check_route(l, 2, score="softmax", bias=torch.tensor([b, 0.0, 0.0], device="cuda"))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_route_masks(score, with_bias):
+    inf, low32, low16 = float("inf"), torch.finfo(torch.float32).min, torch.finfo(torch.bfloat16).min
+    l = _logits(10, 48, 7)
+    l[0] = -inf
+    l[1] = low32
+    l[2] = low16
+    l[3] = float("nan")
+    l[4, 3:] = -inf
+    l[5, ::2] = float("nan")
+    l[6, 5] = inf
+    l[7, 9] = l[7, 30] = inf
+    l[8, :16] = low32
+    l[9, 1:] = -1e38          # finite, far below: open
+    kw = dict(score=score)
+    if with_bias:
+        kw["bias"] = wl.random_matrix(1, 48, 8, std=0.5)[0].cuda()
+    check_route(l, 5, **kw)
+    check_route(l, 5, renormalize=False, **kw)
+    check_route(l, 5, groups=6, top_groups=3, group_top=1, **kw)
+    check_route(l, 5, groups=6, top_groups=3, group_top=2, **kw)
+    b = l.bfloat16()          # the lowest fp32 value becomes -inf
+    check_route(b, 5, **kw)
+
+
+def test_route_small_scores_keep_their_proportions():
+    l = torch.tensor([[200.0, -100.0, -101.0, -300.0, -301.5]], device="cuda")
+    bias = torch.tensor([-9.0, 0.0, 0.0, 5.0, 5.0], device="cuda")
+    check_route(l, 2, score="softmax", bias=bias)
+    check_route(l, 2, score="sigmoid", bias=bias)
+
+
+def test_route_refusals():
+    l = _logits(2, 8, 1)
+    for kw, err in ((dict(score="relu"), ValueError), (dict(bias=torch.zeros(7, device="cuda")), ValueError),
+                    (dict(bias=torch.zeros(8)), TypeError), (dict(groups=3), w4.W4A8Error),
+                    (dict(ids=torch.zeros(2, 2, device="cuda")), TypeError),
+                    (dict(weights=torch.zeros(2, 3, device="cuda")), TypeError)):
+        with pytest.raises(err):
+            w4.w4a8_moe_route(l, 2, **kw)
+    for bad in (l.half(), l.t(), l[:, ::2], l[0]):
+        with pytest.raises(TypeError):
+            w4.w4a8_moe_route(bad, 2)
+    ids, w = w4.w4a8_moe_route(l[:0], 2)
+    assert ids.shape == w.shape == (0, 2)
+
+
+# --------------------------------------------------------------- dispatch
+
+def _ids(M, k, E, seed, drop=0.0):
+    r = np.random.RandomState(seed)
+    ids = np.stack([r.permutation(E)[:k] if k <= E else r.randint(0, E, k) for _ in range(M)])
+    ids = ids.reshape(M, k)
+    bad = np.array([-1, E, E + 7, -(1 << 31), (1 << 31) - 1])
+    where = r.rand(M, k) < drop
+    return np.where(where, bad[r.randint(0, 5, (M, k))], ids).astype(np.int32)
+
+
+def check_dispatch(X, ids, E, flags=0):
+    M, K = X.shape
+    n = ids.size
+    out = w4.MoEDispatch(torch.full((n, K), 77, dtype=torch.int8, device="cuda"),
+                         torch.full((n,), -5.0, device="cuda"),
+                         torch.full((E + 1,), -9, dtype=torch.int32, device="cuda"),
+                         torch.full((n,), -9, dtype=torch.int32, device="cuda"),
+                         torch.full(ids.shape, -9, dtype=torch.int32, device="cuda"))
+    d = w4.w4a8_moe_dispatch(X, torch.from_numpy(ids).cuda(), E, out=out, flags=flags)
+    assert d is out
+    offsets, rows, pos = plain.places(ids, E)
+    used = len(rows)
+    assert np.array_equal(d.offsets.cpu().numpy(), offsets)
+    assert np.array_equal(d.pos.cpu().numpy(), pos)
+    assert np.array_equal(d.rows.cpu().numpy()[:used], rows)
+    Xq, sx = oracle.quantize_act(X.float().cpu().numpy())
+    tok = rows // ids.shape[1]
+    assert np.array_equal(d.Xq.cpu().numpy()[:used], Xq[tok])
+    assert np.array_equal(d.s_x.cpu().numpy()[:used], sx[tok])
+    # rows behind the last expert's are as they were
+    assert torch.all(d.Xq[used:] == 77) and torch.all(d.s_x[used:] == -5.0)
+    assert torch.all(d.rows[used:] == -9)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K,k,E,drop", [
+    (1, 4096, 2, 8, 0.0), (1, 16, 1, 1, 0.0), (3, 48, 32, 40, 0.2), (5, 8192, 3, 1024, 0.1),
+    (64, 128, 8, 64, 1.0), (256, 272, 8, 33, 0.3),          # 2048 pairs: one launch
+    (257, 272, 8, 33, 0.3), (2049, 16, 1, 5, 0.0),          # two launches, one grouping CTA
+    (700, 512, 6, 64, 0.25), (1500, 64, 9, 1024, 0.1),      # a grouping cluster
+    (4111, 128, 4, 7, 0.0), (3, 16384, 2, 8, 0.0), (2100, 8208, 1, 3, 0.5)])
+def test_dispatch(M, K, k, E, drop, dtype):
+    X = wl.random_matrix(M, K, 400 + M, std=1.0, kind="rowzero").to(dtype).cuda()
+    check_dispatch(X, _ids(M, k, E, M + k, drop), E)
+
+
+def test_dispatch_one_expert_twice_and_rounding_ties():
+    X = wl.random_matrix(40, 256, 11, std=1.0, kind="ties").cuda()
+    ids = np.full((40, 3), 2, np.int32)
+    ids[::5, 1] = 0
+    check_dispatch(X, ids, 4)
+    # scales outside the range of the reciprocal form
+    X = wl.random_matrix(6, 128, 12)
+    X[0] *= 1e-30
+    X[1] *= 1e30
+    X[2] *= 1e-38
+    check_dispatch(X.cuda(), _ids(6, 2, 4, 3), 4)
+    check_dispatch(X.cuda(), _ids(6, 2, 4, 3), 4, flags=w4.W4A8_FLAG_PDL)
+
+
+def test_dispatch_of_no_tokens_and_refusals():
+    X = torch.zeros(0, 128, device="cuda")
+    d = w4.w4a8_moe_dispatch(X, torch.zeros(0, 2, dtype=torch.int32, device="cuda"), 4)
+    assert d.offsets.tolist() == [0] * 5 and d.Xq.shape == (0, 128)
+    X = torch.zeros(4, 128, device="cuda")
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    for x, i in ((X.half(), ids), (X[:, ::2], ids), (X, ids.long()), (X, ids.t())):
+        with pytest.raises(TypeError):
+            w4.w4a8_moe_dispatch(x, i, 4)
+    with pytest.raises(ValueError):
+        w4.w4a8_moe_dispatch(X, ids[:3], 4)
+    with pytest.raises(ValueError):
+        w4.w4a8_moe_dispatch(X, ids, 0)
+    with pytest.raises(w4.W4A8Error):
+        w4.w4a8_moe_dispatch(X, ids, 1025)
+    with pytest.raises(TypeError):
+        w4.w4a8_moe_dispatch(X, ids, 4, out=w4.w4a8_moe_dispatch(X, ids, 5))
+
+
+# ---------------------------------------------------------------- combine
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,k,R", [(1, 4096, 2, 2), (5, 1, 1, 7), (7, 2049, 3, 11),
+                                     (3, 8, 32, 40), (33, 264, 9, 100), (12, 2056, 8, 96)])
+def test_combine(M, N, k, R, dtype):
+    r = np.random.RandomState(M + N)
+    Y = wl.random_matrix(R, N, 500 + N).bfloat16().cuda()
+    pos = r.randint(-2, R + 2, (M, k)).astype(np.int32)
+    pos[0] = -1 if M > 1 else pos[0]
+    w = r.rand(M, k).astype(np.float32)
+    check_combine(Y, pos, w, dtype)
+
+
+def check_combine(Y, pos, w, dtype, out=None):
+    got = w4.w4a8_moe_combine(Y, torch.from_numpy(pos).cuda(), torch.from_numpy(w).cuda(),
+                              dtype=dtype, out=out)
+    assert got.dtype == dtype
+    ref, mag = plain.combine(Y.float().cpu().numpy(), pos, w)
+    # k products and sums in fp32, each half a step of the terms' sum at most,
+    # then half a step of the output's type
+    tol = pos.shape[1] * 2.0 ** -23 * mag
+    if dtype == torch.bfloat16:
+        tol += 2.0 ** -8 * (np.abs(ref) + tol)
+    assert np.all(np.abs(got.double().cpu().numpy() - ref) <= tol)
+
+
+def test_combine_unaligned_buffers():
+    Y = wl.random_matrix(9 * 64 + 1, 1, 3).bfloat16().cuda().view(-1)[1:].view(9, 64)
+    assert Y.data_ptr() % 16 != 0
+    pos = np.arange(8, dtype=np.int32).reshape(4, 2)
+    w = np.full((4, 2), 0.5, np.float32)
+    check_combine(Y, pos, w, torch.float32)
+    buf = torch.zeros(4 * 64 + 1, dtype=torch.bfloat16, device="cuda")
+    check_combine(Y.clone(), pos, w, torch.bfloat16, out=buf[1:].view(4, 64))
+    assert buf[0] == 0
+
+
+def test_combine_refusals():
+    Y = torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    w = torch.zeros(2, 2, device="cuda")
+    for a in ((Y.float(), pos, w), (Y, pos.long(), w), (Y, pos, w.double()), (Y.t(), pos, w)):
+        with pytest.raises(TypeError):
+            w4.w4a8_moe_combine(*a)
+    with pytest.raises(ValueError):
+        w4.w4a8_moe_combine(Y, pos, w[:, :1].contiguous())
+    with pytest.raises(TypeError):
+        w4.w4a8_moe_combine(Y, pos, w, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        w4.w4a8_moe_combine(Y, pos, w, out=torch.zeros(2, 9, device="cuda"))
+    # no rows at all, and no tokens
+    out = w4.w4a8_moe_combine(Y[:0], pos, w)
+    assert out.shape == (2, 8) and not out.any()
+    assert w4.w4a8_moe_combine(Y, pos[:0], w[:0]).shape == (0, 8)
+
+
+# ------------------------------------------------------- the layer together
+
+def _layer(X, logits, gw, k, E, out, flags, **kw):
+    ids, w = w4.w4a8_moe_route(logits, k, flags=flags, **kw)
+    d = w4.w4a8_moe_dispatch(X, ids, E, flags=flags)
+    Y = torch.zeros(d.Xq.shape[0], gw.N, dtype=torch.bfloat16, device="cuda")
+    w4.w4a8_grouped_gemm(d.Xq, d.s_x, gw, d.offsets, max_rows=X.shape[0], out=Y, flags=flags)
+    return w4.w4a8_moe_combine(Y, d.pos, w, out=out, flags=flags), ids, w, d, Y
+
+
+@pytest.mark.parametrize("M,k,E,local", [(1, 2, 8, 8), (37, 2, 8, 8), (300, 4, 12, 9)])
+def test_moe_layer(M, k, E, local):
+    """Route, dispatch, grouped GEMM, combine; with local < E the experts from
+    there on live elsewhere and their slots are dropped."""
+    N, K = 384, 512
+    X = wl.random_matrix(M, K, 600 + M)
+    logits = wl.random_matrix(M, E, 601 + M, std=1.5)
+    Ws = [wl.random_matrix(N, K, 602 + e, std=0.02) for e in range(local)]
+    gw = w4.w4a8_quantize_grouped_weights(torch.stack(Ws).cuda())
+    Xd, ld = X.cuda(), logits.cuda()
+    out = torch.empty(M, N, device="cuda")
+    for flags in (0, w4.W4A8_FLAG_PDL):
+        out.fill_(7.0)
+        got, ids, w, d, Y = _layer(Xd, ld, gw, k, local, out, flags)
+        assert got is out
+        ref_ids, ref_w = plain.route(logits.numpy(), k)
+        assert np.array_equal(ids.cpu().numpy(), ref_ids)
+        offsets, rows, pos = plain.places(ref_ids, local)
+        Xq, sx = oracle.quantize_act(X.numpy())
+        tok = rows // k
+        wqs = [oracle.quantize_weights(W.numpy()) for W in Ws]
+        _, y_ref = oracle.w4a8_grouped_gemm(Xq[tok], sx[tok], wqs, offsets.astype(np.int32))
+        assert_bf16_within_1ulp(bf16_bits(Y)[:len(rows)], y_ref)
+        assert not Y[len(rows):].any()
+        ref, mag = plain.combine(Y.float().cpu().numpy(), pos, w.cpu().numpy())
+        assert np.all(np.abs(out.double().cpu().numpy() - ref) <= k * 2.0 ** -23 * mag)
+    assert w4.w4a8_get_status() == 0
+
+
+def test_moe_layer_in_a_graph_and_on_another_stream():
+    """Captured once, replayed for new inputs in the same buffers; and run on
+    a stream of its own while the current one is busy."""
+    M, k, E, N, K = 700, 4, 16, 128, 256
+    g = torch.Generator().manual_seed(9)
+    gw = w4.w4a8_quantize_grouped_weights((torch.randn(E, N, K, generator=g) * 0.02).cuda())
+    inputs = [(torch.randn(M, K, generator=g).cuda(), torch.randn(M, E, generator=g).cuda())
+              for _ in range(3)]
+    X, l = torch.empty_like(inputs[0][0]), torch.empty_like(inputs[0][1])
+    out = torch.empty(M, N, device="cuda")
+    want = [_layer(x, y, gw, k, E, torch.empty_like(out), 0)[0].clone() for x, y in inputs]
+    for flags in (0, w4.W4A8_FLAG_PDL):
+        graph = torch.cuda.CUDAGraph()
+        X.copy_(inputs[0][0])
+        l.copy_(inputs[0][1])
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            _layer(X, l, gw, k, E, out, flags)
+        for (x, y), ref in zip(inputs, want):
+            X.copy_(x)
+            l.copy_(y)
+            graph.replay()
+            assert torch.equal(out, ref)
+        del graph
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    junk = torch.randn(2048, 2048, device="cuda")
+    for _ in range(5):
+        junk = junk @ junk * 1e-2
+    got = []
+    for x, y in inputs:
+        ids, w = w4.w4a8_moe_route(y, k, stream=s)
+        d = w4.w4a8_moe_dispatch(x, ids, E, stream=s)
+        with torch.cuda.stream(s):
+            Y = w4.w4a8_grouped_gemm(d.Xq, d.s_x, gw, d.offsets, max_rows=M)
+        got.append(w4.w4a8_moe_combine(Y, d.pos, w, dtype=torch.float32, stream=s))
+    s.synchronize()
+    for a, ref in zip(got, want):
+        assert torch.equal(a, ref)
+    torch.cuda.synchronize()

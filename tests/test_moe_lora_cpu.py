@@ -1,0 +1,147 @@
+"""Host-only checks of the mixture-of-experts token operators and the low-rank
+adapters: refusals before any launch, and the 64-bit statements the GPU tests
+compare with, against brute force."""
+import numpy as np
+import pytest
+import torch
+
+import bit_block_quantized_w4a8_b200 as w4
+from bit_block_quantized_w4a8_b200 import build as wbuild
+import moe_plain as plain
+
+
+@pytest.fixture(scope="module")
+def L():
+    wbuild.build()
+    return w4.lib()
+
+
+P = 1 << 20  # an aligned address that is never read
+
+
+def test_route_refusals(L):
+    def call(M=4, E=8, k=2, type=0, score=0, groups=1, top_groups=1, group_top=1, flags=0,
+             logits=None, bias=None):
+        return L.w4a8_moe_route(logits, type, M, E, k, score, bias, groups, top_groups, group_top,
+                                1, 1.0, None, None, flags, None)
+    assert call(M=0) == w4.OK
+    assert call() == w4.ERR_INVALID_ARG                   # no logits
+    assert call(M=-1) == w4.ERR_INVALID_ARG
+    assert call(M=0, flags=2) == w4.ERR_INVALID_ARG
+    assert call(M=0, type=2) == w4.ERR_INVALID_ARG
+    assert call(M=0, score=2) == w4.ERR_INVALID_ARG
+    assert call(M=0, group_top=3) == w4.ERR_INVALID_ARG
+    assert call(M=0, k=9) == w4.ERR_INVALID_ARG           # more than the experts
+    assert call(M=0, k=0) == w4.ERR_INVALID_ARG
+    assert call(M=0, E=9, groups=2) == w4.ERR_INVALID_ARG  # uneven groups
+    assert call(M=0, groups=4, top_groups=5) == w4.ERR_INVALID_ARG
+    assert call(M=0, groups=4, top_groups=1, k=3) == w4.ERR_INVALID_ARG  # closed experts
+    assert call(M=0, E=1024) == w4.OK
+    assert call(M=0, E=1025) == w4.ERR_UNSUPPORTED_SHAPE
+    assert call(M=0, E=64, k=33) == w4.ERR_UNSUPPORTED_SHAPE
+    assert call(M=0, E=66, groups=33, k=1) == w4.ERR_UNSUPPORTED_SHAPE
+    assert call(M=0, E=1024, groups=32, top_groups=2, k=32) == w4.OK
+    assert call(M=0, E=5 * 129, groups=5, k=1) == w4.ERR_UNSUPPORTED_SHAPE
+    assert call(M=0, E=5 * 128, groups=5, k=1) == w4.OK
+
+
+def test_dispatch_and_combine_refusals(L):
+    def dispatch(M=4, K=128, k=2, E=8, type=0, flags=0, X=P, ids=P, Xq=P, sx=P, off=P, rows=P,
+                 pos=P):
+        return L.w4a8_moe_dispatch(X, type, M, K, ids, k, E, Xq, sx, off, rows, pos, flags, None)
+    assert dispatch(K=120) == w4.ERR_UNSUPPORTED_SHAPE
+    assert dispatch(K=65552) == w4.ERR_UNSUPPORTED_SHAPE
+    assert dispatch(k=33) == w4.ERR_UNSUPPORTED_SHAPE
+    assert dispatch(E=1025) == w4.ERR_UNSUPPORTED_SHAPE
+    assert dispatch(M=1 << 29, k=4) == w4.ERR_UNSUPPORTED_SHAPE
+    for bad in (dict(M=-1), dict(k=0), dict(E=0), dict(type=3), dict(flags=2), dict(X=None),
+                dict(ids=None), dict(Xq=None), dict(sx=None), dict(off=None), dict(rows=None),
+                dict(pos=None)):
+        assert dispatch(**bad) == w4.ERR_INVALID_ARG, bad
+    for bad in (dict(X=P + 8), dict(Xq=P + 8), dict(ids=P + 2), dict(off=P + 1), dict(pos=P + 2)):
+        assert dispatch(**bad) == w4.ERR_MISALIGNED, bad
+
+    def combine(M=4, N=64, k=2, rows=8, type=1, flags=0, Y=P, pos=P, w=P, out=P):
+        return L.w4a8_moe_combine(Y, rows, N, pos, w, M, k, out, type, flags, None)
+    assert combine(M=0, Y=None) == w4.OK
+    assert combine(k=33) == w4.ERR_UNSUPPORTED_SHAPE
+    for bad in (dict(M=-1), dict(N=0), dict(k=0), dict(rows=-1), dict(type=5), dict(flags=4),
+                dict(Y=None), dict(pos=None), dict(w=None), dict(out=None)):
+        assert combine(**bad) == w4.ERR_INVALID_ARG, bad
+    for bad in (dict(Y=P + 1), dict(pos=P + 2), dict(w=P + 2), dict(out=P + 1),
+                dict(out=P + 2, type=0)):
+        assert combine(**bad) == w4.ERR_MISALIGNED, bad
+
+
+def test_lora_refusals(L):
+    def call(M=4, K=256, N=64, r=16, ad=3, type=0, ldx=None, ldy=None, X=P, A=P, B=P, scale=None,
+             ids=P, off=None, rows=None, Y=P, flags=0):
+        return L.w4a8_lora(X, type, K if ldx is None else ldx, M, K, A, B, r, ad, scale, ids, off,
+                           rows, N, Y, N if ldy is None else ldy, flags, None)
+    assert call(M=0, X=None) == w4.OK
+    for bad in (dict(K=200), dict(K=65536 + 128), dict(r=4), dict(r=20), dict(r=136),
+                dict(ad=1025), dict(M=257), dict(M=(1 << 24) + 1, ids=None, off=P, rows=P)):
+        assert call(**bad) == w4.ERR_UNSUPPORTED_SHAPE, bad
+    for bad in (dict(M=-1), dict(N=0), dict(r=0), dict(ad=0), dict(type=2), dict(ldx=255),
+                dict(ldy=63), dict(X=None), dict(A=None), dict(B=None), dict(Y=None),
+                dict(ids=None), dict(ids=None, off=P), dict(off=P, rows=P), dict(flags=2)):
+        assert call(**bad) == w4.ERR_INVALID_ARG, bad
+    for bad in (dict(X=P + 4), dict(ldx=258), dict(ldx=260, type=1), dict(A=P + 8), dict(B=P + 8),
+                dict(Y=P + 1), dict(scale=P + 2), dict(ids=P + 2)):
+        assert call(**bad) == w4.ERR_MISALIGNED, bad
+
+    def planned(M=4, ad=3, ids=P, off=P, rows=P, flags=0):
+        return L.w4a8_lora_plan(ids, M, ad, off, rows, flags, None)
+    assert planned(ad=1025) == w4.ERR_UNSUPPORTED_SHAPE
+    for bad in (dict(M=-1), dict(ad=0), dict(ids=None), dict(off=None), dict(rows=None),
+                dict(flags=2)):
+        assert planned(**bad) == w4.ERR_INVALID_ARG, bad
+    assert planned(rows=P + 2) == w4.ERR_MISALIGNED
+
+
+def test_cpu_tensors_are_refused():
+    x, i = torch.zeros(2, 128), torch.zeros(2, 1, dtype=torch.int32)
+    y = torch.zeros(2, 8, dtype=torch.bfloat16)
+    for call in (lambda: w4.w4a8_moe_route(x, 2), lambda: w4.w4a8_moe_dispatch(x, i, 4),
+                 lambda: w4.w4a8_moe_combine(y, i, x[:, :1]),
+                 lambda: w4.w4a8_lora_plan(i[:, 0], 4),
+                 lambda: w4.w4a8_lora(x, y, y[None], y[None], i[:, 0])):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    class T:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="and cuda:1"):
+        w4._together(None, T(0), T(1))
+    with pytest.raises(ValueError, match="current device"):
+        w4._together(None, T(1), None, T(1))
+    with pytest.raises(ValueError, match="stream on"):
+        w4._together(T(1), T(0))
+
+
+def test_plain_route_by_hand():
+    ids, w = plain.route([[1.0, 3.0, 2.0, 3.0]], 3)
+    assert ids.tolist() == [[1, 3, 2]]
+    e = np.exp(np.array([3.0, 3.0, 2.0]))
+    assert np.allclose(w, e / e.sum())
+    # the bias moves the choice, not the weights
+    ids, w = plain.route([[0.0, 1.0, 2.0]], 1, "sigmoid", bias=[9.0, 0.0, 0.0], renormalize=False)
+    assert ids.tolist() == [[0]] and np.allclose(w, 0.5)
+    # groups by their two best: (4, 0) against (3, 3)
+    ids, _ = plain.route([[4.0, 0.0, 3.0, 3.0]], 2, "sigmoid", groups=2, group_top=2)
+    assert ids.tolist() == [[2, 3]]
+    ids, _ = plain.route([[4.0, 0.0, 3.0, 3.0]], 2, "sigmoid", groups=2, group_top=1)
+    assert ids.tolist() == [[0, 1]]
+    # nothing left, and half of it left
+    ids, w = plain.route([[-np.inf, np.nan], [-np.inf, 5.0]], 2)
+    assert ids.tolist() == [[-1, -1], [1, -1]] and w.tolist() == [[0, 0], [1, 0]]
+
+
+def test_plain_places_by_hand():
+    off, rows, pos = plain.places(np.array([[2, 0], [0, -1], [2, 7]]), 3)
+    assert off.tolist() == [0, 2, 2, 4] and rows.tolist() == [1, 2, 0, 4]
+    assert pos.tolist() == [[2, 0], [1, -1], [3, -1]]
