@@ -460,17 +460,33 @@ def _typed(t, ndim, name):
 
 def _together(stream, first, *others):
     """All tensors on one device, which has to be the current one (the
-    kernels are launched there), and the stream's handle."""
-    d = first.device
+    kernels are launched there), and the stream's handle.  The current stream
+    is asked for its bare handle: making a Stream object of it takes 3 us,
+    a third of a small call."""
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != d:
-            raise ValueError("tensors on %s and %s" % (d, t.device))
-    if d.index != _torch.cuda.current_device():
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors on %s and %s" % (first.device, t.device))
+    if d != _torch.cuda.current_device():
         raise ValueError("tensors on %s, but the current device is cuda:%d"
-                         % (d, _torch.cuda.current_device()))
-    if stream is not None and stream.device != d:
-        raise ValueError("tensors on %s, stream on %s" % (d, stream.device))
-    return _stream(stream)
+                         % (first.device, _torch.cuda.current_device()))
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(d)
+    if stream.device.index != d:
+        raise ValueError("tensors on %s, stream on %s" % (first.device, stream.device))
+    return stream.cuda_stream
+
+
+def _is(t, dtype, shape, d):
+    """Whether t is a contiguous tensor of this type and shape on CUDA device d."""
+    return (isinstance(t, _torch.Tensor) and t.dtype == dtype and t.shape == shape
+            and t.get_device() == d and t.is_contiguous())
+
+
+def _need_out(t, dtype, shape, d, name):
+    if not _is(t, dtype, shape, d):
+        raise TypeError("%s must be a contiguous %s tensor of shape %s on cuda:%d" %
+                        (name, dtype, tuple(shape), d))
 
 
 def _new(stream, shape, dtype, device):
@@ -507,14 +523,20 @@ def w4a8_moe_route(logits, top_k, score="softmax", bias=None, groups=1, top_grou
     if k < 1:
         raise ValueError("top_k must be positive")
     st = _together(stream, logits, bias)
-    ids = (_new(stream, (M, k), _torch.int32, logits.device) if ids is None
-           else _out(ids, _torch.int32, (M, k), logits, "ids"))
-    weights = (_new(stream, (M, k), _torch.float32, logits.device) if weights is None
-               else _out(weights, _torch.float32, (M, k), logits, "weights"))
-    _check(lib().w4a8_moe_route(_ptr(logits), kind, M, E, k, _SCORES[score], _ptr(bias),
-                                int(groups), int(top_groups), int(group_top),
-                                1 if renormalize else 0, float(scale), _ptr(ids), _ptr(weights),
-                                int(flags), st), "w4a8_moe_route")
+    if ids is None:
+        ids = _new(stream, (M, k), _torch.int32, logits.device)
+    else:
+        _need_out(ids, _torch.int32, (M, k), logits.get_device(), "ids")
+    if weights is None:
+        weights = _new(stream, (M, k), _torch.float32, logits.device)
+    else:
+        _need_out(weights, _torch.float32, (M, k), logits.get_device(), "weights")
+    rc = lib().w4a8_moe_route(logits.data_ptr(), kind, M, E, k, _SCORES[score],
+                              None if bias is None else bias.data_ptr(), groups, top_groups,
+                              group_top, 1 if renormalize else 0, scale, ids.data_ptr(),
+                              weights.data_ptr(), flags, st)
+    if rc:
+        _check(rc, "w4a8_moe_route")
     return ids, weights
 
 
@@ -550,14 +572,17 @@ def w4a8_moe_dispatch(X, ids, experts, out=None, stream=None, flags=0):
                           _new(stream, (M * k,), _torch.int32, d),
                           _new(stream, (M, k), _torch.int32, d))
     else:
-        _out(out.Xq, _torch.int8, (M * k, K), X, "out.Xq")
-        _out(out.s_x, _torch.float32, (M * k,), X, "out.s_x")
-        _out(out.offsets, _torch.int32, (E + 1,), X, "out.offsets")
-        _out(out.rows, _torch.int32, (M * k,), X, "out.rows")
-        _out(out.pos, _torch.int32, (M, k), X, "out.pos")
-    _check(lib().w4a8_moe_dispatch(_ptr(X), kind, M, K, _ptr(ids), k, E, _ptr(out.Xq),
-                                   _ptr(out.s_x), _ptr(out.offsets), _ptr(out.rows),
-                                   _ptr(out.pos), int(flags), st), "w4a8_moe_dispatch")
+        d = X.get_device()
+        _need_out(out.Xq, _torch.int8, (M * k, K), d, "out.Xq")
+        _need_out(out.s_x, _torch.float32, (M * k,), d, "out.s_x")
+        _need_out(out.offsets, _torch.int32, (E + 1,), d, "out.offsets")
+        _need_out(out.rows, _torch.int32, (M * k,), d, "out.rows")
+        _need_out(out.pos, _torch.int32, (M, k), d, "out.pos")
+    rc = lib().w4a8_moe_dispatch(X.data_ptr(), kind, M, K, ids.data_ptr(), k, E,
+                                 out.Xq.data_ptr(), out.s_x.data_ptr(), out.offsets.data_ptr(),
+                                 out.rows.data_ptr(), out.pos.data_ptr(), flags, st)
+    if rc:
+        _check(rc, "w4a8_moe_dispatch")
     return out
 
 
@@ -578,9 +603,11 @@ def w4a8_moe_combine(Y, pos, weights, out=None, dtype=_torch.bfloat16, stream=No
         out = _new(stream, (M, N), dtype, Y.device)
     else:
         _typed(out, 2, "out")
-        _out(out, out.dtype, (M, N), Y, "out")
-    _check(lib().w4a8_moe_combine(_ptr(Y), R, N, _ptr(pos), _ptr(weights), M, k, _ptr(out),
-                                  _TYPES[out.dtype], int(flags), st), "w4a8_moe_combine")
+        _need_out(out, out.dtype, (M, N), Y.get_device(), "out")
+    rc = lib().w4a8_moe_combine(Y.data_ptr(), R, N, pos.data_ptr(), weights.data_ptr(), M, k,
+                                out.data_ptr(), _TYPES[out.dtype], flags, st)
+    if rc:
+        _check(rc, "w4a8_moe_combine")
     return out
 
 
@@ -609,10 +636,12 @@ def w4a8_lora_plan(ids, adapters, out=None, stream=None, flags=0):
     else:
         if out.M != M or out.adapters != L:
             raise ValueError("the plan is for %d rows and %d adapters" % (out.M, out.adapters))
-        _out(out.offsets, _torch.int32, (L + 1,), ids, "out.offsets")
-        _out(out.rows, _torch.int32, (M,), ids, "out.rows")
-    _check(lib().w4a8_lora_plan(_ptr(ids), M, L, _ptr(out.offsets), _ptr(out.rows), int(flags),
-                                st), "w4a8_lora_plan")
+        _need_out(out.offsets, _torch.int32, (L + 1,), ids.get_device(), "out.offsets")
+        _need_out(out.rows, _torch.int32, (M,), ids.get_device(), "out.rows")
+    rc = lib().w4a8_lora_plan(ids.data_ptr(), M, L, out.offsets.data_ptr(), out.rows.data_ptr(),
+                              flags, st)
+    if rc:
+        _check(rc, "w4a8_lora_plan")
     return out
 
 
@@ -662,13 +691,17 @@ def w4a8_lora(X, Y, A, B, ids, scale=None, stream=None, flags=0):
         if M > LORA_IDS_MAX:
             # (the second kernel may start early: it waits before it reads)
             plan, ids = w4a8_lora_plan(ids, L, stream=stream, flags=flags), None
-            flags = int(flags) | W4A8_FLAG_PDL
+            flags |= W4A8_FLAG_PDL
     ldx = X.stride(0) if M > 1 else max(X.stride(0), K)
     ldy = Y.stride(0) if M > 1 else max(Y.stride(0), N)
-    _check(lib().w4a8_lora(_ptr(X), kind, ldx, M, K, _ptr(A), _ptr(B), r, L, _ptr(scale),
-                           _ptr(ids), _ptr(plan.offsets) if plan else None,
-                           _ptr(plan.rows) if plan else None, N, _ptr(Y), ldy, int(flags), st),
-           "w4a8_lora")
+    rc = lib().w4a8_lora(X.data_ptr(), kind, ldx, M, K, A.data_ptr(), B.data_ptr(), r, L,
+                         None if scale is None else scale.data_ptr(),
+                         None if ids is None else ids.data_ptr(),
+                         None if plan is None else plan.offsets.data_ptr(),
+                         None if plan is None else plan.rows.data_ptr(), N, Y.data_ptr(), ldy,
+                         flags, st)
+    if rc:
+        _check(rc, "w4a8_lora")
     return Y
 
 

@@ -10,13 +10,17 @@
 // CTA's warps in shared memory and over the cluster through distributed
 // shared memory), then updates its stretch of N.  t never leaves the chip.
 //
-// Bound by HBM (X and Y once, A and B once per adapter and tile, mostly from
-// L2): at ranks up to 64 the tensor work is far below the bytes, so warp
-// level MMAs (m16n8k16) fed straight from global memory carry it.  Both
-// products may sum their index in any order, so each lane takes 8 adjacent
-// elements of a row (16-byte loads) and calls them the four k pairs that its
-// MMA fragments want; the same trick gives each lane 8 adjacent output
-// columns.
+// Bound by HBM (X once, Y twice, A and B once per adapter and tile, mostly
+// from L2): at ranks up to 32 the tensor work is well below the bytes, and
+// warp level MMAs (m16n8k16) carry it.  Both products may sum their index in
+// any order, so each lane takes 8 adjacent elements of a row (16-byte loads)
+// and calls them the four k pairs that its MMA fragments want; the same trick
+// gives each lane adjacent output columns.  All operands pass through one
+// ring of shared memory stages filled by 16-byte asynchronous copies.
+// Loading fragments straight from global memory, two steps ahead in
+// registers, measured 154 us where the ring takes 114 (8192 rows, K = N =
+// 8192, rank 32, fp32 x: 549 MB, 4.8 TB/s); asking A and B into L2 first
+// made a decode batch slower (28 us against 25).
 //
 // Rounding: fp32 activations and t enter the MMAs as two bf16 terms (the
 // value rounded to bf16, and the rest rounded to bf16), which keeps 16
@@ -69,26 +73,64 @@ __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uin
   lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
 }
 
-template <int NT, int WR>
+// The eight warps of a CTA: WR row groups of 16, WK blocks of 32 k (slices of
+// 32 columns in the second product), WN parts of the rank tiles (of a slice's
+// columns).
+template <bool BF16X, int NT, int WR>
 struct LoraCfg {
+  static constexpr int kWarpsN = WR == 1 ? 2 : 1;
+  static constexpr int kWarpsK = kLoraWarps / (WR * kWarpsN);
   static constexpr int kTileRows = 16 * WR;
-  static constexpr int kWarpsK = kLoraWarps / WR;
+  // shared memory: a ring of stages, each WK blocks of 32 k of x and A, or
+  // WK slices of 32 columns of Y and B; then the sums of t
+  static constexpr int kXBytes = kTileRows * kWarpsK * (BF16X ? 64 : 128);
+  static constexpr int kABytes = NT * 8 * kWarpsK * 64;
+  static constexpr int kStageBytes = kXBytes + kABytes;
   static constexpr int kPitch = NT * 8 + 4;  // floats per row of t
   static constexpr int kPartFloats = kTileRows * kPitch;
-  static constexpr int kSmemBytes = (kWarpsK + 1) * kPartFloats * 4;
+  static constexpr int kParts = kWarpsK / 2;
+  static constexpr bool kInPlace = kParts == 1;
+  static constexpr int kSumBytes = (kParts + !kInPlace) * kPartFloats * 4;
+  // two CTAs an SM where each has three stages, and up to six stages each
+  static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 2600 - kSumBytes) / kStageBytes; }
+  static constexpr int kResident = fit(2) >= 3 ? 2 : 1;
+  static constexpr int kStages = fit(kResident) > 6 ? 6 : fit(kResident);
+  static constexpr int kSmemBytes = kStages * kStageBytes + kSumBytes;
+  static_assert(kStages >= 3, "ring");
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 
 // NT: tiles of 8 ranks (ranks past p.rank are zero); WR: tiles of 16 rows.
 template <bool BF16X, int NT, int WR>
-__global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams p) {
-  using C = LoraCfg<NT, WR>;
-  constexpr int TM = C::kTileRows, WK = C::kWarpsK, RP = C::kPitch;
-  extern __shared__ __align__(16) float tsm[];
-  float* part = tsm;                          // [WK][TM][RP]
-  float* full = tsm + WK * C::kPartFloats;    // [TM][RP]
+__global__ void __launch_bounds__(kLoraThreads, LoraCfg<BF16X, NT, WR>::kResident)
+lora_kernel(const LoraParams p) {
+  using C = LoraCfg<BF16X, NT, WR>;
+  constexpr int TM = C::kTileRows, WK = C::kWarpsK, WN = C::kWarpsN, RP = C::kPitch;
+  constexpr int S = C::kStages;
+  extern __shared__ __align__(128) uint8_t lsm[];
+  float* part = reinterpret_cast<float*>(lsm + S * C::kStageBytes);  // [kParts][TM][RP]
+  float* full = part + (C::kInPlace ? 0 : C::kParts) * C::kPartFloats;  // [TM][RP]
+  const uint32_t ring = smem_u32(lsm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int wr = warp % WR, wk = warp / WR;
+  const int wr = warp % WR, wk = warp / WR % WK, wn = warp / (WR * WK);
   const int rank_c = p.ctas > 1 ? (int)cluster_ctarank() : 0;
   const int slot = blockIdx.x / p.ctas;
   pdl_launch_dependents();
@@ -174,101 +216,244 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams 
   // this lane's two rows of the warp's 16
   const int tok[2] = {toks[wr * 16 + g], toks[wr * 16 + g + 8]};
 
-  // ---- t = A x over this CTA's stretch of K, 32 k per step
-  float acc[NT][4];
+  // this CTA's stretches of K (blocks of 32) and of N (slices of 32), WK of
+  // them a stage
+  const int nkb = p.K / 32;
+  const int kb0 = (int)((long long)nkb * rank_c / p.ctas);
+  const int kb1 = (int)((long long)nkb * (rank_c + 1) / p.ctas);
+  const int slices = (p.N + 31) / 32;
+  const int parts = p.ctas * gridDim.y, my = blockIdx.y * p.ctas + rank_c;
+  const int s0 = (int)((long long)slices * my / parts);
+  const int s1 = (int)((long long)slices * (my + 1) / parts);
+  const int n_a = (kb1 - kb0 + WK - 1) / WK, n_b = (s1 - s0 + WK - 1) / WK;
+  const uint16_t* A = p.A + (size_t)adapter * p.rank * p.K;
+  const uint16_t* B = p.B + (size_t)adapter * p.N * p.rank;
+
+  // Copies 16 bytes at a time, a ring of S stages that runs through both
+  // products: the first stages of Y and B arrive while t is summed.  Chunks
+  // of a row sit so that 8 lanes reading two rows meet 8 different bank
+  // groups: in odd rows the halves of each 128 bytes (for fp32 x, whose lanes
+  // take every other chunk, the neighbours) change places; columns of B lie
+  // as they come, with the halves exchanged where their pitch asks for it.
+  // In tall tiles the rows past the tile's last copy its first, unread.
+  // What a thread copies keeps its place from stage to stage, so the
+  // addresses are found once and advance by a constant.
+  constexpr int XC = WK * (BF16X ? 4 : 8), HC = WK * 4;  // chunks of a row: x; A and Y
+  constexpr int XS = kLoraThreads / XC, HS = kLoraThreads / HC;  // rows apart
+  constexpr int XI = TM / XS, YI = TM / HS;
+  static_assert(XI * XS == TM && YI * HS == TM && XS % 2 == 0 && HS % 2 == 0, "copies");
+  const int xrow = tid / XC, xch = tid % XC, hrow = tid / HC, hch = tid % HC;
+  const uint32_t xto = (xrow * XC + (BF16X ? xch ^ ((xrow & 1) * 4) : xch ^ (xrow & 1))) * 16;
+  const uint32_t hto = (hrow * HC + (hch ^ ((hrow & 1) * 4))) * 16;
+  const int rc = p.rank / 8;  // chunks of a column of B
+  const int flip = rc == 8 ? 3 : rc == 16 ? 4 : 31;  // the bit of a chunk's index that tells odd columns
+  const uint8_t* xp[XI];
+  const uint8_t* yq[YI];
+  unsigned xin = 0, yin = 0;
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int i = 0; i < XI; ++i) {
+    int m = toks[xrow + i * XS];
+    if (WR > 1 && m < 0) m = toks[0];
+    if (m >= 0) xin |= 1u << i;
+    xp[i] = static_cast<const uint8_t*>(p.X) +
+            ((size_t)max(m, 0) * p.ldx + 32 * kb0) * (BF16X ? 2 : 4) + xch * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < YI; ++i) {
+    int m = toks[hrow + i * HS];
+    if (WR > 1 && m < 0) m = toks[0];
+    if (m >= 0 && p.y_vec) yin |= 1u << i;
+    yq[i] = reinterpret_cast<const uint8_t*>(p.Y + (size_t)max(m, 0) * p.ldy + 32 * s0) + hch * 16;
+  }
+  const uint8_t* ap = reinterpret_cast<const uint8_t*>(A + (size_t)hrow * p.K + 32 * kb0) + hch * 16;
+  const uint8_t* bp = reinterpret_cast<const uint8_t*>(B + (size_t)32 * s0 * p.rank) + tid * 16;
+  int ahead = 0;          // the next stage to copy,
+  uint32_t st_in = ring;  // and where it goes
+  auto issue = [&]() {
+    if (ahead < n_a) {
+      const int left = kb1 - kb0 - ahead * WK;  // blocks
+      if (xch < left * (BF16X ? 4 : 8)) {
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+          if (WR > 1 || (xin >> i & 1)) cp_async16(st_in + xto + i * 4096, xp[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < XI; ++i) xp[i] += XC * 16;
+      if (hch < left * 4) {
+#pragma unroll
+        for (int i = 0; i < (NT * 8 + HS - 1) / HS; ++i)
+          if (hrow + i * HS < p.rank)
+            cp_async16(st_in + C::kXBytes + hto + i * 4096, ap + (size_t)i * HS * p.K * 2);
+      }
+      ap += HC * 16;
+    } else if (ahead < n_a + n_b) {
+      const int n = (s0 + (ahead - n_a) * WK) * 32;
+      const int cols = min(min(WK * 32, s1 * 32 - n), p.N - n);
+      if (hch * 8 + 8 <= cols && p.y_vec) {
+#pragma unroll
+        for (int i = 0; i < YI; ++i)
+          if (WR > 1 || (yin >> i & 1)) cp_async16(st_in + hto + i * 4096, yq[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < YI; ++i) yq[i] += HC * 16;
+      const int chunks = cols * rc;
+#pragma unroll
+      for (int i = 0; i < (WK * 32 * NT + kLoraThreads - 1) / kLoraThreads; ++i) {
+        const int at = tid + i * kLoraThreads;
+        if (at < chunks)
+          cp_async16(st_in + C::kXBytes + (at ^ ((at >> flip & 1) * 4)) * 16, bp + i * 4096);
+      }
+      bp += WK * 64 * p.rank;
+    }
+    cp_async_commit();
+    ++ahead;
+    st_in += C::kStageBytes;
+    if (st_in == ring + S * C::kStageBytes) st_in = ring;
+  };
+#pragma unroll 1
+  for (int t = 0; t < S - 1; ++t) issue();
+
+  // ---- t = A x over this CTA's stretch of K: the warp's rows and block of
+  // k, and its NW rank tiles.  What was not copied (rows past cnt, ranks
+  // past p.rank) is read all the same: it can only reach those rows and
+  // ranks of t, which the sums below leave out.
+  constexpr int NW = NT / WN;
+  float acc[NW][4];
+#pragma unroll
+  for (int j = 0; j < NW; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-  {
-    const int nkb = p.K / 32;
-    const int kb1 = (int)((long long)nkb * (rank_c + 1) / p.ctas);
-    const uint16_t* Aw = p.A + ((size_t)adapter * p.rank + g) * p.K + 8 * c;
-    const int nt = p.rank / 8;
-    for (int kb = (int)((long long)nkb * rank_c / p.ctas) + wk; kb < kb1; kb += WK) {
-      const int k = kb * 32;
-      uint4 b[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        b[j] = make_uint4(0, 0, 0, 0);
-        if (j < nt) b[j] = __ldg(reinterpret_cast<const uint4*>(Aw + (size_t)(8 * j) * p.K + k));
-      }
+  const int odd = g & 1;  // of this lane's rows, in every matrix
+  const int nt = p.rank / 8 - wn * NW;
+  const uint32_t x_at = (wr * 16 + g) * XC * 16 +
+                        (BF16X ? (wk * 4 + c) ^ (odd * 4) : wk * 8 + 2 * c + odd) * 16;
+  const uint32_t h_at = ((wk * 4 + c) ^ (odd * 4)) * 16;
+  const uint32_t a_at = C::kXBytes + (wn * NW * 8 + g) * HC * 16 + h_at;
+  uint32_t st = ring;
+  auto next = [&]() {
+    cp_async_wait<S - 2>();
+    __syncthreads();
+    issue();
+  };
+  auto done = [&]() {
+    st += C::kStageBytes;
+    if (st == ring + S * C::kStageBytes) st = ring;
+  };
+#pragma unroll 1
+  for (int kb = kb0 + wk; kb < kb0 + wk + n_a * WK; kb += WK) {
+    next();
+    if (kb < kb1) {
       // hi and lo words: [row half][k pair]
       uint32_t hi[2][4], lo[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const uint32_t x = st + x_at + h * 8 * XC * 16;
+        const uint4 u = lds128(x);
         if constexpr (BF16X) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (tok[h] >= 0)
-            v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.X) +
-                                                     (size_t)tok[h] * p.ldx + k + 8 * c));
-          hi[h][0] = v.x;
-          hi[h][1] = v.y;
-          hi[h][2] = v.z;
-          hi[h][3] = v.w;
+          hi[h][0] = u.x;
+          hi[h][1] = u.y;
+          hi[h][2] = u.z;
+          hi[h][3] = u.w;
         } else {
-          float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-          if (tok[h] >= 0) {
-            const float4* x = reinterpret_cast<const float4*>(
-                static_cast<const float*>(p.X) + (size_t)tok[h] * p.ldx + k + 8 * c);
-            u = __ldg(x);
-            v = __ldg(x + 1);
-          }
-          split_bf16(u.x, u.y, hi[h][0], lo[h][0]);
-          split_bf16(u.z, u.w, hi[h][1], lo[h][1]);
-          split_bf16(v.x, v.y, hi[h][2], lo[h][2]);
-          split_bf16(v.z, v.w, hi[h][3], lo[h][3]);
+          const uint4 v = lds128(x ^ 16);
+          split_bf16(__uint_as_float(u.x), __uint_as_float(u.y), hi[h][0], lo[h][0]);
+          split_bf16(__uint_as_float(u.z), __uint_as_float(u.w), hi[h][1], lo[h][1]);
+          split_bf16(__uint_as_float(v.x), __uint_as_float(v.y), hi[h][2], lo[h][2]);
+          split_bf16(__uint_as_float(v.z), __uint_as_float(v.w), hi[h][3], lo[h][3]);
         }
       }
+      // (a tile's MMAs depend on one another: four tiles take turns)
+      constexpr int JB = NW < 4 ? NW : 4;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (j >= nt) continue;
-        mma_bf16(acc[j], hi[0][0], hi[1][0], hi[0][1], hi[1][1], b[j].x, b[j].y);
-        mma_bf16(acc[j], hi[0][2], hi[1][2], hi[0][3], hi[1][3], b[j].z, b[j].w);
+      for (int j0 = 0; j0 < NW; j0 += JB) {
+        if (j0 >= nt) continue;
+        uint4 w[JB];
+#pragma unroll
+        for (int j = 0; j < JB; ++j) w[j] = lds128(st + a_at + (j0 + j) * 8 * HC * 16);
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+          mma_bf16(acc[j0 + j], hi[0][0], hi[1][0], hi[0][1], hi[1][1], w[j].x, w[j].y);
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+          mma_bf16(acc[j0 + j], hi[0][2], hi[1][2], hi[0][3], hi[1][3], w[j].z, w[j].w);
         if constexpr (!BF16X) {
-          mma_bf16(acc[j], lo[0][0], lo[1][0], lo[0][1], lo[1][1], b[j].x, b[j].y);
-          mma_bf16(acc[j], lo[0][2], lo[1][2], lo[0][3], lo[1][3], b[j].z, b[j].w);
+#pragma unroll
+          for (int j = 0; j < JB; ++j)
+            mma_bf16(acc[j0 + j], lo[0][0], lo[1][0], lo[0][1], lo[1][1], w[j].x, w[j].y);
+#pragma unroll
+          for (int j = 0; j < JB; ++j)
+            mma_bf16(acc[j0 + j], lo[0][2], lo[1][2], lo[0][3], lo[1][3], w[j].z, w[j].w);
         }
       }
     }
+    done();
   }
+
+  // Sums over the warps' stretches of K, then over the cluster's, each in a
+  // fixed order.  The upper half of the warps lays its sums down, the lower
+  // half adds its own.
   {
-    float* mine = part + wk * C::kPartFloats + (wr * 16 + g) * RP + 2 * c;
+    float* mine = part + (wk % C::kParts) * C::kPartFloats + (wr * 16 + g) * RP +
+                  wn * NW * 8 + 2 * c;
+    if (wk >= C::kParts) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      *reinterpret_cast<float2*>(mine + 8 * j) = make_float2(acc[j][0], acc[j][1]);
-      *reinterpret_cast<float2*>(mine + 8 * RP + 8 * j) = make_float2(acc[j][2], acc[j][3]);
+      for (int j = 0; j < NW; ++j) {
+        *reinterpret_cast<float2*>(mine + 8 * j) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2*>(mine + 8 * RP + 8 * j) = make_float2(acc[j][2], acc[j][3]);
+      }
     }
+    __syncthreads();
+    if (wk < C::kParts) {
+#pragma unroll
+      for (int j = 0; j < NW; ++j) {
+        float2* u = reinterpret_cast<float2*>(mine + 8 * j);
+        float2* v = reinterpret_cast<float2*>(mine + 8 * RP + 8 * j);
+        *u = make_float2(acc[j][0] + u->x, acc[j][1] + u->y);
+        *v = make_float2(acc[j][2] + v->x, acc[j][3] + v->y);
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  // sums over the warps' stretches of K, then over the cluster's, each in a
-  // fixed order; ranks past p.rank and rows past cnt are zero already
   const float s = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
-  for (int i = tid; i < TM * NT * 8; i += kLoraThreads) {
-    const int at = i / (NT * 8) * RP + i % (NT * 8);
-    float v = part[at];
+  if (p.ctas > 1 && C::kParts > 1) {
+    for (int i = tid; i < cnt * NT * 8; i += kLoraThreads) {
+      const int at = i / (NT * 8) * RP + i % (NT * 8);
+      float v = part[at];
 #pragma unroll
-    for (int w = 1; w < WK; ++w) v += part[w * C::kPartFloats + at];
-    if (p.ctas > 1)
+      for (int w = 1; w < C::kParts; ++w) v += part[w * C::kPartFloats + at];
       part[at] = v;
-    else
-      full[at] = v * s;
-  }
-  if (p.ctas > 1) {
-    cluster_sync_all();
-    for (int i = tid; i < TM * NT * 8; i += kLoraThreads) {
-      const int r = i / (NT * 8), at = r * RP + i % (NT * 8);
-      float v = 0.0f;
-      if (r < cnt)
-        for (int q = 0; q < p.ctas; ++q)
-          v += __int_as_float(dsmem_ld_s32(dsmem_map(smem_u32(part + at), q)));
-      full[at] = v * s;
     }
-    cluster_arrive();  // this CTA has read its peers' sums
+  }
+  if (p.ctas > 1) cluster_sync_all();
+  // (with one part the totals take its place, so every CTA of the cluster has
+  // to be done reading first)
+  constexpr int EI = TM * NT * 8 / kLoraThreads;
+  float sum[EI];
+#pragma unroll
+  for (int e = 0; e < EI; ++e) {
+    const int i = tid + e * kLoraThreads;
+    const int r = i / (NT * 8), at = r * RP + i % (NT * 8);
+    sum[e] = 0.0f;
+    if (r < cnt && i % (NT * 8) < p.rank) {
+      if (p.ctas > 1) {
+        for (int q = 0; q < p.ctas; ++q)
+          sum[e] += __int_as_float(dsmem_ld_s32(dsmem_map(smem_u32(part + at), q)));
+      } else {
+#pragma unroll
+        for (int w = 0; w < C::kParts; ++w) sum[e] += part[w * C::kPartFloats + at];
+      }
+    }
+  }
+  if (p.ctas > 1) cluster_arrive();
+  if (p.ctas > 1 && C::kInPlace) cluster_wait();
+#pragma unroll
+  for (int e = 0; e < EI; ++e) {
+    const int i = tid + e * kLoraThreads;
+    full[i / (NT * 8) * RP + i % (NT * 8)] = sum[e] * s;
   }
   __syncthreads();
 
-  // ---- Y += t B^T over this CTA's stretch of N, 32 columns per step
+  // ---- Y += t B^T over this CTA's stretch of N
   constexpr int KW = NT == 2 ? 4 : 8;   // adjacent ranks per lane
   constexpr int NB = NT * 8 / (4 * KW); // rank blocks
   uint32_t th[NB][2][KW / 2], tl[NB][2][KW / 2];
@@ -282,89 +467,115 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_kernel(const LoraParams 
             full + (wr * 16 + g + 8 * h) * RP + b * 4 * KW + KW * c + 2 * i);
         split_bf16(v.x, v.y, th[b][h][i], tl[b][h][i]);
       }
-  const int slices = (p.N + 31) / 32;
-  const int parts = p.ctas * gridDim.y, my = blockIdx.y * p.ctas + rank_c;
-  const int s1 = (int)((long long)slices * (my + 1) / parts);
-  const uint16_t* Bw = p.B + (size_t)adapter * p.N * p.rank + KW * c;
-  const int jcol = (g >> 1) * 8 + (g & 1);  // + 2 q: the column of MMA column g, n tile q
-  for (int sl = (int)((long long)slices * my / parts) + wk; sl < s1; sl += WK) {
-    const int n = sl * 32, col = n + 8 * c;
-    uint16_t* yp[2];
-    uint4 y[2];
-    const bool whole = p.y_vec && col + 8 <= p.N;
+  // a lane's CW adjacent columns are those of QN column tiles
+  constexpr int QN = 4 / WN, CW = 2 * QN, YW = QN;  // YW: words of a row of Y
+  const int jcol = wn * 16 + (g >> 1) * CW + odd;   // + 2 q: the column of MMA column g, tile q
+  const int ycol = wn * 16 + CW * c;                // this lane's first column
+  const uint32_t y_at = (wr * 16 + g) * HC * 16 +
+                        ((wk * 4 + ycol / 8) ^ (odd * 4)) * 16 + (ycol % 8) * 2;
+  const int b_at = (wk * 32 + jcol) * rc;           // chunk
+  // (a lane past p.rank, where t is zero, reads its column's first chunk)
+  int b_ch[NB];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      yp[h] = p.Y + (size_t)(tok[h] < 0 ? 0 : tok[h]) * p.ldy + col;
-      y[h] = make_uint4(0, 0, 0, 0);
-      if (tok[h] >= 0) {
-        if (whole) {
-          y[h] = *reinterpret_cast<const uint4*>(yp[h]);
-        } else {
-          uint32_t w[4] = {0, 0, 0, 0};
+  for (int b = 0; b < NB; ++b)
+    b_ch[b] = (b * 4 * KW + KW * c < p.rank) ? 4 * b * KW / 8 + (KW == 8 ? c : 0) : 0;
+  const int b_flip = flip < 31 ? odd * 4 : 0;
+  const uint32_t b_step = 2 * rc * 16;
+  const uint32_t b_sub = KW == 4 && KW * c < p.rank ? c * 8 : 0;
+  uint16_t* yrow[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (col + i < p.N) w[i / 2] |= (uint32_t)yp[h][i] << (16 * (i & 1));
-          y[h] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-    }
-    float d[4][4];
+  for (int h = 0; h < 2; ++h) yrow[h] = p.Y + (size_t)max(tok[h], 0) * p.ldy;
+#pragma unroll 1
+  for (int sl = s0 + wk; sl < s0 + wk + n_b * WK; sl += WK) {
+    next();
+    if (sl < s1) {
+      const int col = sl * 32 + ycol;
+      const bool whole = p.y_vec && (col & ~7) + 8 <= p.N;
+      float d[QN][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w[4] = {y[h].x, y[h].y, y[h].z, y[h].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        d[q][2 * h] = __uint_as_float(w[q] << 16);
-        d[q][2 * h + 1] = __uint_as_float(w[q] & 0xffff0000u);
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const bool in = b * 4 * KW + KW * c < p.rank;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int bc = n + jcol + 2 * q;
-        uint32_t w[KW / 2];
-        const uint16_t* src = Bw + (size_t)bc * p.rank + b * 4 * KW;
-        if constexpr (KW == 8) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (in && bc < p.N) v = __ldg(reinterpret_cast<const uint4*>(src));
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[YW];
+        const uint32_t at = st + y_at + h * 8 * HC * 16;
+        if constexpr (YW == 4) {
+          const uint4 v = lds128(at);
           w[0] = v.x;
           w[1] = v.y;
           w[2] = v.z;
           w[3] = v.w;
         } else {
-          uint2 v = make_uint2(0, 0);
-          if (in && bc < p.N) v = __ldg(reinterpret_cast<const uint2*>(src));
+          const uint2 v = lds64(at);
           w[0] = v.x;
           w[1] = v.y;
         }
+        if (!whole) {
+#pragma unroll
+          for (int q = 0; q < YW; ++q) {
+            w[q] = 0;
+            if (tok[h] >= 0 && col + 2 * q < p.N) w[q] = yrow[h][col + 2 * q];
+            if (tok[h] >= 0 && col + 2 * q + 1 < p.N)
+              w[q] |= (uint32_t)yrow[h][col + 2 * q + 1] << 16;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < QN; ++q) {
+          d[q][2 * h] = __uint_as_float(w[q] << 16);
+          d[q][2 * h + 1] = __uint_as_float(w[q] & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t w[QN][KW / 2];
+        // (the columns' parity, and so the exchange of halves, is the lane's)
+        const uint32_t ad = st + C::kXBytes + ((b_at + b_ch[b]) ^ b_flip) * 16 + b_sub;
+#pragma unroll
+        for (int q = 0; q < QN; ++q) {
+          if constexpr (KW == 8) {
+            const uint4 v = lds128(ad + q * b_step);
+            w[q][0] = v.x;
+            w[q][1] = v.y;
+            w[q][2] = v.z;
+            w[q][3] = v.w;
+          } else {
+            const uint2 v = lds64(ad + q * b_step);
+            w[q][0] = v.x;
+            w[q][1] = v.y;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < KW / 2; i += 2) {
-          mma_bf16(d[q], th[b][0][i], th[b][1][i], th[b][0][i + 1], th[b][1][i + 1], w[i],
-                   w[i + 1]);
-          mma_bf16(d[q], tl[b][0][i], tl[b][1][i], tl[b][0][i + 1], tl[b][1][i + 1], w[i],
-                   w[i + 1]);
+#pragma unroll
+          for (int q = 0; q < QN; ++q)
+            mma_bf16(d[q], th[b][0][i], th[b][1][i], th[b][0][i + 1], th[b][1][i + 1], w[q][i],
+                     w[q][i + 1]);
+#pragma unroll
+          for (int q = 0; q < QN; ++q)
+            mma_bf16(d[q], tl[b][0][i], tl[b][1][i], tl[b][0][i + 1], tl[b][1][i + 1], w[q][i],
+                     w[q][i + 1]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (tok[h] < 0) continue;
+        uint32_t w[YW];
+#pragma unroll
+        for (int q = 0; q < QN; ++q) w[q] = pack_bf16(d[q][2 * h], d[q][2 * h + 1]);
+        uint16_t* yp = yrow[h] + col;
+        if (whole) {
+          if constexpr (YW == 4)
+            *reinterpret_cast<uint4*>(yp) = make_uint4(w[0], w[1], w[2], w[3]);
+          else
+            *reinterpret_cast<uint2*>(yp) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < CW; ++i)
+            if (col + i < p.N) yp[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
         }
       }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (tok[h] < 0) continue;
-      const uint32_t w[4] = {pack_bf16(d[0][2 * h], d[0][2 * h + 1]),
-                             pack_bf16(d[1][2 * h], d[1][2 * h + 1]),
-                             pack_bf16(d[2][2 * h], d[2][2 * h + 1]),
-                             pack_bf16(d[3][2 * h], d[3][2 * h + 1])};
-      if (whole) {
-        *reinterpret_cast<uint4*>(yp[h]) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (col + i < p.N) yp[h][i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-      }
-    }
+    done();
   }
-  if (p.ctas > 1) cluster_wait();  // nobody still reads this CTA's sums
+  cp_async_wait<0>();
+  if (p.ctas > 1 && !C::kInPlace) cluster_wait();  // nobody still reads this CTA's sums
 }
 
 }  // namespace w4a8

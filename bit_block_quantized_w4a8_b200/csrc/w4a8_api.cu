@@ -981,7 +981,7 @@ cudaError_t launch_combine(const uint16_t* Y, int rows, int N, const int* pos,
 template <bool BF16X, int NT, int WR>
 cudaError_t launch_lora_as(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
   static std::atomic<bool> done[kMaxDevices];
-  constexpr int smem = LoraCfg<NT, WR>::kSmemBytes;
+  constexpr int smem = LoraCfg<BF16X, NT, WR>::kSmemBytes;
   const cudaError_t e = ensure_smem(lora_kernel<BF16X, NT, WR>, smem, done);
   if (e != cudaSuccess) return e;
   return launch_k(lora_kernel<BF16X, NT, WR>, dim3(slots * p.ctas, parts), dim3(kLoraThreads), smem,
@@ -996,18 +996,19 @@ cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream
   return launch_lora_as<BF16X, 16, WR>(p, slots, parts, st, pdl);
 }
 
-// Row tiles of 64 where adapters have that many rows on average, else of 16;
-// a tile's cluster and the further split of N grow until the CTAs cover the
-// machine twice, while a CTA keeps a k step per warp and 8 column slices.
+// Row tiles of 64 where adapters have 32 rows or more on average, else of 16;
+// a tile's cluster, then the further split of N, grow while the CTAs still
+// fit the machine at once, two an SM (one more doubling is a second wave:
+// 32 rows of 32 adapters, K = 8192, N = 10240, rank 64, take 20 us with 256
+// CTAs, 30 with 512, 35 with 64), a CTA keeping 256 k and 128 columns.
 cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool pdl) {
   const int used = p.adapters < p.M ? p.adapters : p.M;
   const bool tall = p.M / used >= 32;
   const int tm = tall ? 64 : 16;
   const int slots = (int)(((long long)p.M + (long long)used * (tm - 1)) / tm);
-  const int wk = tall ? kLoraWarps / 4 : kLoraWarps;
   int ctas = 1, parts = 1;
-  while (ctas < 8 && (long long)slots * ctas < 2 * sms && p.K / 32 >= 2 * ctas * wk) ctas *= 2;
-  while ((long long)slots * ctas * parts < 2 * sms && p.N / 32 >= 2 * ctas * parts * 8) parts *= 2;
+  while (ctas < 8 && (long long)slots * ctas * 2 <= 2 * sms && p.K >= 512 * ctas) ctas *= 2;
+  while ((long long)slots * ctas * parts * 2 <= 2 * sms && p.N >= 256 * ctas * parts) parts *= 2;
   p.ctas = ctas;
   if (tall)
     return bf16x ? launch_lora_nt<true, 4>(p, slots, parts, st, pdl)
