@@ -20,43 +20,61 @@ namespace w4a8 {
 // of the logits IS the order of the scores and no arithmetic can blur it.
 // With a bias (or when a group is scored by the sum of its two best) the keys
 // are sums of a score and a number, and two of them can be closer than fp32
-// tells apart; they are computed in fp64, whose units on this chip run at half
-// the fp32 rate, so that the chosen experts are those of the definition.
+// tells apart.  They are first computed in fp32 with an error bound; only if
+// two keys that decide something lie within it does the warp do the token
+// again with fp64 keys (a few tokens in a thousand), so that the chosen
+// experts are always those of the definition.  fp64 keys for every token
+// measured 23.5 us for 8191 tokens of 256 experts in 8 groups, this 12.4.
 // Weights are fp32.
 //
 // Layout.  The lanes are divided evenly among the groups (rounded up to a
-// power of two), so a group's score is a few shuffles among its own lanes
-// for all groups at once; with one group every lane holds every 32nd expert.
+// power of two), each lane holding NV adjacent experts, so a group's score is
+// a few shuffles among its own lanes for all groups at once, and logits come
+// in wide loads.
+//
+// Rounds.  A lane keeps its two or three best keys at hand, as few lanes win
+// more often; one that does looks through its experts again, on its own.
 constexpr int kRouteWarps = 4;
 constexpr float kMaskedLogit = -3.3895313892515355e38f;  // bf16's lowest finite value
 
 struct RouteParams {
   const void* logits;
   int bf16;             // logits type: 0 = fp32, 1 = bf16
+  int vec;              // wide loads: runs of 16 bytes (or NV elements) of a group are aligned
+  int vec_bias;         // the same for the bias, 16 bytes
   int M, E, k;
   int sigmoid;
   const float* bias;    // [E] or nullptr
   int groups, top_groups, group_top;
+  int group_size;       // E / groups
   int lanes_per_group;  // power of two, lanes_per_group * ceil2(groups) = 32
+  int lanes_shift;      // its logarithm
   int renormalize;
   float scale;
   int* ids;
   float* weights;
 };
 
-__device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 and +0 are one value
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
 __device__ __forceinline__ uint64_t order_key(double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);  // -0 and +0 are one value
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
-// warp maximum of a key: one redux for 32 bits, two for 64
-__device__ __forceinline__ uint32_t warp_max_key(uint32_t v) {
-  return __reduce_max_sync(0xffffffffu, v);
+// the number of an order_key
+__device__ __forceinline__ double key_value(uint64_t k) {
+  return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
-__device__ __forceinline__ uint64_t warp_max_key(uint64_t v) {
+// Warp maxima and minima in one instruction (two for 64 bits).
+__device__ __forceinline__ float warp_max_redux(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_min_redux(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t warp_max_redux(uint64_t v) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
   const uint32_t lo = __reduce_max_sync(
       0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
@@ -73,43 +91,203 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// MODE 0: logit keys, groups (if any) scored by their best logit;
-// MODE 1: logit keys, groups scored by sums of two fp64 scores;
-// MODE 2: fp64 keys score + bias.
-template <int MODE> struct RouteKey { using type = uint32_t; };
-template <> struct RouteKey<2> { using type = uint64_t; };
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp_approx(float x) {
+  return ex2_approx(x * 1.4426950408889634f);
+}
 
-template <int NV, int MODE>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
-  using Key = typename RouteKey<MODE>::type;
-  constexpr uint32_t kFull = 0xffffffffu;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long m = (long long)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
-  if (m >= p.M) return;
-  const int lg = p.lanes_per_group;
-  const int sub = lane & (lg - 1), grp = lane / lg;
-  const int size = p.E / p.groups;
-  const int e0 = grp * size + sub;
-  const float* lf = static_cast<const float*>(p.logits) + m * p.E;
-  const __nv_bfloat16* lb = static_cast<const __nv_bfloat16*>(p.logits) + m * p.E;
-  float l[NV];
-  float mx = -INFINITY;
+// Keys of the choice.  fp32: the numbers themselves, -inf = masked.  fp64:
+// integers in the numbers' order, 0 = masked.
+template <typename Key> struct KeyOf;
+template <> struct KeyOf<float> {
+  static __device__ __forceinline__ float none() { return -INFINITY; }
+};
+template <> struct KeyOf<uint64_t> {
+  static __device__ __forceinline__ uint64_t none() { return 0; }
+};
+
+// The D best of a lane's keys that come after expert `eb` with key `kb` in
+// the order of choice (larger keys first, then lower indexes), and their
+// experts, best first.
+template <int NV, int D, bool ALL, typename Key>
+__device__ __forceinline__ void best_of(const Key (&key)[NV], int e0, Key kb, int eb, Key (&bk)[D],
+                                        int (&be)[D]) {
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    bk[d] = KeyOf<Key>::none();
+    be[d] = e0;
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const bool in = grp < p.groups && sub + i * lg < size;
-    float v = -INFINITY;
-    if (in) v = p.bf16 ? __bfloat162float(lb[e0 + i * lg]) : lf[e0 + i * lg];
-    l[i] = v > kMaskedLogit ? v : -INFINITY;  // (false for NaN)
-    mx = fmaxf(mx, l[i]);
+    Key k = key[i];
+    if (!ALL && !(k < kb || (k == kb && e0 + i > eb))) k = KeyOf<Key>::none();
+#pragma unroll
+    for (int d = D - 1; d >= 0; --d) {
+      const bool here = k > bk[d], above = d > 0 && k > bk[d > 0 ? d - 1 : 0];
+      be[d] = above ? be[d > 0 ? d - 1 : 0] : here ? e0 + i : be[d];
+      bk[d] = above ? bk[d > 0 ? d - 1 : 0] : here ? k : bk[d];
+    }
   }
-  mx = warp_max(mx);
+}
 
-  // the softmax's denominator, where something needs it
-  double inv_sum = 1.0;
-  float sum_f = 1.0f;
+// k rounds: the largest key, the lowest expert among equals; lane j keeps the
+// j-th choice.  With CHECK, false as soon as two keys that follow one another
+// (the first that is not chosen among them) are not `margin` apart.
+template <int NV, bool CHECK, typename Key>
+__device__ __forceinline__ bool take_best(const Key (&key)[NV], int k, int e0, float margin,
+                                          int lane, int& mine) {
+  constexpr int D = NV < 2 ? 1 : NV < 8 ? 2 : 3;  // keys at hand
+  const Key none = KeyOf<Key>::none();
+  mine = -1;
+  Key bk[D], last = none;
+  int be[D];
+  best_of<NV, D, true, Key>(key, e0, none, 0, bk, be);
+  for (int j = 0;; ++j) {
+    if (!CHECK && j == k) break;
+    const Key top = warp_max_redux(bk[0]);
+    if (!(top > none)) break;  // nothing is left
+    if constexpr (CHECK) {
+      if (j > 0 && !((float)last - (float)top > margin)) return false;
+      if (j == k) break;
+      last = top;
+    }
+    const int e =
+        (int)__reduce_min_sync(0xffffffffu, bk[0] == top ? (uint32_t)be[0] : 0xffffffffu);
+    if (lane == j) mine = e;
+    if (be[0] == e && bk[0] == top) {  // one lane
+#pragma unroll
+      for (int d = 0; d + 1 < D; ++d) {
+        bk[d] = bk[d + 1];
+        be[d] = be[d + 1];
+      }
+      bk[D - 1] = none;
+      if (NV > D && !(bk[0] > none))
+        best_of<NV, D, false, Key>(key, e0, top, e, bk, be);
+    }
+    __syncwarp();
+  }
+  return true;
+}
+
+// MODE 0: logit keys, groups (if any) scored by their best logit;
+// MODE 1: logit keys, groups scored by sums of two scores;
+// MODE 2: keys score + bias.
+//
+// The first try, in fp32; false where it is not certain.  What a score can be
+// off by: e^x as 2^(x log2 e) by the hardware's approximation has a relative
+// error of 2^-22 and that of its argument, |x| 2^-23, and |x| e^-|x| < 0.4;
+// with an approximate reciprocal (2^-23) a sigmoid is within 2^-21.  (What
+// these flush to zero is below 2^-126.)  A softmax adds its sum's error, 37
+// additions.  A sum of such a number with a bias, or of two, is rounded to
+// 2^-24 of it.  `margin` covers a pair of them.
+template <int NV, int MODE>
+__device__ __forceinline__ bool route_choose(const RouteParams& p, const float (&l)[NV], float mx,
+                                             int lane, int& mine) {
+  constexpr uint32_t kFull = 0xffffffffu;
+  const int lg = p.lanes_per_group, size = p.group_size;
+  const int sub = lane & (lg - 1), grp = lane >> p.lanes_shift;
+  const int e0 = grp * size + sub * NV;
+  float margin = p.sigmoid ? 0x1p-19f : 0x1p-17f;
+  float inv_sum = 1.0f;
   if (MODE != 0 && !p.sigmoid) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      s += l[i] > -INFINITY ? (l[i] == mx ? 1.0f : exp_approx(l[i] - mx)) : 0.0f;
+    s = warp_sum(s);
+    inv_sum = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
+  }
+  float sc[NV];  // scores; -inf = masked
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (MODE == 0) continue;
+    const float v = p.sigmoid ? rcp_approx(1.0f + ex2_approx(l[i] * -1.4426950408889634f))
+                              : (l[i] == mx ? inv_sum : exp_approx(l[i] - mx) * inv_sum);
+    sc[i] = l[i] > -INFINITY ? v : -INFINITY;
+  }
+  float key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) key[i] = l[i];
+  if constexpr (MODE == 2) {
+    const int left = grp < p.groups ? size - sub * NV : 0;
+    float b[NV];
+    float big = 0.0f;
+    if (NV >= 4 && p.vec_bias) {
+#pragma unroll
+      for (int i = 0; i < NV; i += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < left) v = __ldg(reinterpret_cast<const float4*>(p.bias + e0 + i));
+        b[i] = v.x;
+        b[(i + 1) % NV] = v.y;
+        b[(i + 2) % NV] = v.z;
+        b[(i + 3) % NV] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) b[i] = i < left ? __ldg(p.bias + e0 + i) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      big = fmaxf(big, fabsf(b[i]));
+      key[i] = l[i] > -INFINITY ? sc[i] + b[i] : -INFINITY;
+    }
+    margin *= 1.0f + warp_max_redux(big);
+  }
+  if (p.groups > 1) {
+    // the group's two best (a missing one is -inf)
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float v = MODE == 1 ? sc[i] : key[i];
+      if (MODE != 0) b = fmaxf(b, fminf(a, v));
+      a = fmaxf(a, v);
+    }
+    for (int o = lg / 2; o > 0; o >>= 1) {
+      const float a2 = __shfl_xor_sync(kFull, a, o);
+      if (MODE != 0) {
+        const float b2 = __shfl_xor_sync(kFull, b, o);
+        b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+      }
+      a = fmaxf(a, a2);
+    }
+    if (MODE != 0 && p.group_top == 2 && b > -INFINITY) a += b;
+    int before = 0;
+    for (int h = 0; h < p.groups; ++h) {
+      const float o = __shfl_sync(kFull, a, h * lg);
+      before += o > a || (o == a && h < grp);
+    }
+    const bool open = before < p.top_groups && grp < p.groups;
+    if constexpr (MODE != 0) {
+      // the last open group and the best closed one
+      const float lo = warp_min_redux(open ? a : INFINITY);
+      const float hi = warp_max_redux(open || grp >= p.groups ? -INFINITY : a);
+      if (hi > -INFINITY && !(lo - hi > 2.0f * margin)) return false;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = open ? key[i] : -INFINITY;
+  }
+  return take_best<NV, MODE == 2, float>(key, p.k, e0, margin, lane, mine);
+}
+
+// The same with scores, their sums and the keys of MODE 2 in fp64.
+template <int NV, int MODE>
+__device__ __forceinline__ void route_choose_exact(const RouteParams& p, const float (&l)[NV],
+                                                   float mx, int lane, int& mine) {
+  constexpr uint32_t kFull = 0xffffffffu;
+  const int lg = p.lanes_per_group, size = p.group_size;
+  const int sub = lane & (lg - 1), grp = lane >> p.lanes_shift;
+  const int e0 = grp * size + sub * NV;
+  double inv_sum = 1.0;
+  if (!p.sigmoid) {
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -117,119 +295,154 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     s = warp_sum(s);
     inv_sum = s > 0.0 ? 1.0 / s : 0.0;
   }
+  auto score = [&](float x) -> double {  // x unmasked
+    if (p.sigmoid) return 1.0 / (1.0 + exp(-(double)x));
+    return x == mx ? inv_sum : exp((double)x - (double)mx) * inv_sum;
+  };
+  // MODE 1 takes experts by their logits, exact as they are
+  uint64_t key[NV];
+  double a = -INFINITY, b = -INFINITY;  // the group's two best
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    key[i] = 0;
+    if (!(l[i] > -INFINITY)) continue;
+    double v = score(l[i]);
+    if (MODE == 2) v += (double)__ldg(p.bias + e0 + i);
+    key[i] = order_key(MODE == 2 ? v : (double)l[i]);
+    if (v > a) {
+      b = a;
+      a = v;
+    } else if (v > b) {
+      b = v;
+    }
+  }
+  if (p.groups > 1) {
+    for (int o = lg / 2; o > 0; o >>= 1) {
+      const double a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+      b = fmax(fmin(a, a2), fmax(b, b2));
+      a = fmax(a, a2);
+    }
+    if (p.group_top == 2 && b > -INFINITY) a += b;
+    int before = 0;
+    for (int h = 0; h < p.groups; ++h) {
+      const double o = __shfl_sync(kFull, a, h * lg);
+      before += o > a || (o == a && h < grp);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (before >= p.top_groups) key[i] = 0;
+  }
+  take_best<NV, false, uint64_t>(key, p.k, e0, 0.0f, lane, mine);
+}
+
+template <int NV, int MODE>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long m = (long long)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (m >= p.M) return;
+  const int lg = p.lanes_per_group, size = p.group_size;
+  const int sub = lane & (lg - 1), grp = lane >> p.lanes_shift;
+  const int e0 = grp * size + sub * NV;
+  const float* lf = static_cast<const float*>(p.logits) + m * p.E;
+  const uint16_t* lb = static_cast<const uint16_t*>(p.logits) + m * p.E;
+  const int left = grp < p.groups ? size - sub * NV : 0;  // this lane's experts
+  float l[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) l[i] = -INFINITY;
+  if (p.vec && p.bf16) {
+    constexpr int W = NV < 8 ? NV : 8;
+#pragma unroll
+    for (int i = 0; i < NV; i += W) {
+      if (i >= left) continue;
+      uint32_t u[4] = {0, 0, 0, 0};
+      if constexpr (W == 8) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(lb + e0 + i));
+        u[0] = v.x;
+        u[1] = v.y;
+        u[2] = v.z;
+        u[3] = v.w;
+      } else if constexpr (W == 4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(lb + e0 + i));
+        u[0] = v.x;
+        u[1] = v.y;
+      } else if constexpr (W == 2) {
+        u[0] = __ldg(reinterpret_cast<const uint32_t*>(lb + e0 + i));
+      } else {
+        u[0] = __ldg(lb + e0 + i);
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        l[i + w] = __uint_as_float(w & 1 ? u[w / 2] & 0xffff0000u : u[w / 2] << 16);
+    }
+  } else if (p.vec) {
+    constexpr int W = NV < 4 ? NV : 4;
+#pragma unroll
+    for (int i = 0; i < NV; i += W) {
+      if (i >= left) continue;
+      if constexpr (W == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(lf + e0 + i));
+        l[i] = v.x;
+        l[i + 1] = v.y;
+        l[i + 2] = v.z;
+        l[i + 3] = v.w;
+      } else if constexpr (W == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(lf + e0 + i));
+        l[i] = v.x;
+        l[i + 1] = v.y;
+      } else {
+        l[i] = __ldg(lf + e0 + i);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i < left)
+        l[i] = p.bf16 ? __uint_as_float((uint32_t)__ldg(lb + e0 + i) << 16) : __ldg(lf + e0 + i);
+  }
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    l[i] = l[i] > kMaskedLogit ? l[i] : -INFINITY;  // (false for NaN)
+    mx = fmaxf(mx, l[i]);
+  }
+  mx = warp_max_redux(mx);
+  float sum = 1.0f;
   if (!p.renormalize && !p.sigmoid) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (l[i] > -INFINITY) s += l[i] == mx ? 1.0f : expf(l[i] - mx);
-    sum_f = warp_sum(s);
-  }
-  auto score = [&](float x) -> double {  // x unmasked
-    if (p.sigmoid) return 1.0 / (1.0 + exp(-(double)x));
-    return x == mx ? inv_sum : exp((double)x - (double)mx) * inv_sum;
-  };
-
-  Key key[NV];  // 0 = masked
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    key[i] = 0;
-    if (l[i] > -INFINITY) {
-      if constexpr (MODE == 2)
-        key[i] = order_key(score(l[i]) + (double)__ldg(p.bias + e0 + i * lg));
-      else
-        key[i] = order_key(l[i]);
-    }
+    sum = warp_sum(s);
   }
 
-  if (p.groups > 1) {
-    uint64_t gkey = 0;  // 0 = no expert of the group is left
-    if constexpr (MODE == 0) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) gkey = max(gkey, (uint64_t)key[i]);
-      for (int o = lg / 2; o > 0; o >>= 1)
-        gkey = max(gkey, (uint64_t)__shfl_xor_sync(kFull, (uint32_t)gkey, o));
-    } else {
-      // the two best scores of the group (a missing one is -inf)
-      double a = -INFINITY, b = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (!(l[i] > -INFINITY)) continue;
-        double v;
-        if constexpr (MODE == 2) {
-          const uint64_t u = key[i];  // the key is the score's bits
-          v = __longlong_as_double((long long)((u >> 63) ? u & 0x7fffffffffffffffull : ~u));
-        } else {
-          v = score(l[i]);
-        }
-        if (v > a) {
-          b = a;
-          a = v;
-        } else if (v > b) {
-          b = v;
-        }
-      }
-      for (int o = lg / 2; o > 0; o >>= 1) {
-        const double a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
-        const double hi = fmax(a, a2), lo = fmin(a, a2);
-        b = fmax(lo, a == hi ? b : b2);
-        a = hi;
-      }
-      if (a > -INFINITY) gkey = order_key(p.group_top == 2 && b > -INFINITY ? a + b : a);
-    }
-    int before = 0;
-    for (int h = 0; h < p.groups; ++h) {
-      const uint64_t o = __shfl_sync(kFull, gkey, h * lg);
-      before += o > gkey || (o == gkey && h < grp);
-    }
-    if (before >= p.top_groups) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = 0;
-    }
-  }
-
-  // k rounds: the largest key, the lowest expert among equals.  Lane j keeps
-  // the j-th choice.
-  int mine = -1;
-  for (int j = 0; j < p.k; ++j) {
-    Key best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    const Key top = warp_max_key(best);
-    if (top == 0) break;  // nothing is left
-    const uint32_t e = __reduce_min_sync(
-        kFull, best == top ? (uint32_t)(e0 + at * lg) : 0xffffffffu);
-    if (lane == j) mine = (int)e;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (best == top && (uint32_t)(e0 + i * lg) == e) key[i] = 0;
+  int mine;
+  if (!route_choose<NV, MODE>(p, l, mx, lane, mine)) {
+    if constexpr (MODE != 0) route_choose_exact<NV, MODE>(p, l, mx, lane, mine);
   }
 
   // weights: lane j holds the j-th choice's logit
   const bool has = mine >= 0;
   float x = -INFINITY;
-  if (has) x = p.bf16 ? __bfloat162float(lb[mine]) : lf[mine];
+  if (has) x = p.bf16 ? __uint_as_float((uint32_t)__ldg(lb + mine) << 16) : __ldg(lf + mine);
   float w = 0.0f;
   if (!p.sigmoid) {
     // renormalised: relative to the largest chosen logit, so that chosen
     // experts far below the row's maximum keep their proportions
-    const float ref = p.renormalize ? warp_max(x) : mx;
+    const float ref = p.renormalize ? warp_max_redux(x) : mx;
     if (has) w = x == ref ? 1.0f : expf(x - ref);
-    const float s = p.renormalize ? warp_sum(w) : sum_f;
-    if (has) w = w / s;
+    const float s = p.renormalize ? warp_sum(w) : sum;
+    if (has) w = __fdividef(w, s);
   } else {
     // sigmoid(x) = exp(min(x, 0)) / (1 + exp(-|x|)); the renormalised form
     // takes the largest chosen exponent out of both sides
     const float t = fminf(x, 0.0f);
-    const float ref = p.renormalize ? warp_max(t) : 0.0f;
-    if (has) w = (t == ref ? 1.0f : expf(t - ref)) / (1.0f + expf(-fabsf(x)));
+    const float ref = p.renormalize ? warp_max_redux(t) : 0.0f;
+    if (has) w = __fdividef(t == ref ? 1.0f : expf(t - ref), 1.0f + expf(-fabsf(x)));
     if (p.renormalize) {
       const float s = warp_sum(w);
-      if (has) w = w / s;
+      if (has) w = __fdividef(w, s);
     }
   }
   if (lane < p.k) {

@@ -935,14 +935,22 @@ cudaError_t launch_route_nv(const RouteParams& p, int mode, cudaStream_t st, boo
   return launch_k(route_kernel<NV, 2>, grid, block, 0, st, pdl, 1, p);
 }
 
-cudaError_t launch_route(const RouteParams& p, int mode, cudaStream_t st, bool pdl) {
-  const int nv = (p.E / p.groups + p.lanes_per_group - 1) / p.lanes_per_group;
-  if (nv <= 1) return launch_route_nv<1>(p, mode, st, pdl);
-  if (nv <= 2) return launch_route_nv<2>(p, mode, st, pdl);
-  if (nv <= 4) return launch_route_nv<4>(p, mode, st, pdl);
-  if (nv <= 8) return launch_route_nv<8>(p, mode, st, pdl);
-  if (nv <= 16) return launch_route_nv<16>(p, mode, st, pdl);
-  return launch_route_nv<32>(p, mode, st, pdl);
+cudaError_t launch_route(RouteParams p, int mode, cudaStream_t st, bool pdl) {
+  const int size = p.E / p.groups;
+  const int nv = (size + p.lanes_per_group - 1) / p.lanes_per_group;
+  int held = 1;  // experts per lane, a power of two
+  while (held < nv) held *= 2;
+  const int run = p.bf16 ? (held < 8 ? held : 8) : (held < 4 ? held : 4);  // elements a load
+  p.vec = size % run == 0 && aligned(p.logits, run * (p.bf16 ? 2 : 4));
+  p.vec_bias = size % 4 == 0 && aligned(p.bias, 16);
+  switch (held) {
+    case 1: return launch_route_nv<1>(p, mode, st, pdl);
+    case 2: return launch_route_nv<2>(p, mode, st, pdl);
+    case 4: return launch_route_nv<4>(p, mode, st, pdl);
+    case 8: return launch_route_nv<8>(p, mode, st, pdl);
+    case 16: return launch_route_nv<16>(p, mode, st, pdl);
+    default: return launch_route_nv<32>(p, mode, st, pdl);
+  }
 }
 
 // One CTA groups up to kGroupOneCta ids; more take a cluster.
@@ -1272,7 +1280,10 @@ int w4a8_moe_route(const void* logits, int logits_type, int M, int E, int top_k,
   p.groups = groups;
   p.top_groups = top_groups;
   p.group_top = group_top;
+  p.group_size = E / groups;
   p.lanes_per_group = lanes;
+  p.lanes_shift = 0;
+  while ((1 << p.lanes_shift) < lanes) ++p.lanes_shift;
   p.renormalize = renormalize != 0;
   p.scale = scale;
   p.ids = ids;
