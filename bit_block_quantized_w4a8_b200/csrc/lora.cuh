@@ -436,8 +436,12 @@ lora_kernel(const LoraParams p) {
     sum[e] = 0.0f;
     if (r < cnt && i % (NT * 8) < p.rank) {
       if (p.ctas > 1) {
-        for (int q = 0; q < p.ctas; ++q)
-          sum[e] += __int_as_float(dsmem_ld_s32(dsmem_map(smem_u32(part + at), q)));
+        float v[8];  // (all at once: a load from another CTA takes its time)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          v[q] = q < p.ctas ? __int_as_float(dsmem_ld_s32(dsmem_map(smem_u32(part + at), q))) : 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[e] += v[q];
       } else {
 #pragma unroll
         for (int w = 0; w < C::kParts; ++w) sum[e] += part[w * C::kPartFloats + at];

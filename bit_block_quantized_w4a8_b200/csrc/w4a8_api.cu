@@ -953,28 +953,52 @@ cudaError_t launch_route(RouteParams p, int mode, cudaStream_t st, bool pdl) {
   }
 }
 
-// One CTA groups up to kGroupOneCta ids; more take a cluster.
-constexpr int kGroupOneCta = 4096;
+// One CTA groups up to kGroupOneCta ids; more take a cluster (4096 ids: 5.4
+// us by one CTA, 4.7 by a cluster; 2048: 3.6 by one).
+constexpr int kGroupOneCta = 2048;
+
+template <bool WORDS>
+cudaError_t launch_group_rows_as(const int* ids, int n, int groups, int* offsets, int* rows,
+                                 int* pos, cudaStream_t st, bool pdl) {
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = ensure_smem(group_rows_kernel<WORDS>,
+                                    group_rows_smem(WORDS ? kGroupWords : kMaxGroups), done);
+  if (e != cudaSuccess) return e;
+  const int ctas = n > kGroupOneCta ? kGroupCluster : 1;
+  int bits = 1;
+  while (groups >> bits) ++bits;  // of an id, or of `groups`, which stands for none
+  return launch_k(group_rows_kernel<WORDS>, dim3(ctas), dim3(kGroupThreads),
+                  group_rows_smem(groups), st, pdl, ctas, ids, n, groups, bits, ctas, offsets,
+                  rows, pos);
+}
 
 cudaError_t launch_group_rows(const int* ids, int n, int groups, int* offsets, int* rows, int* pos,
                               cudaStream_t st, bool pdl) {
-  static std::atomic<bool> done[kMaxDevices];
-  const cudaError_t e = ensure_smem(group_rows_kernel, group_rows_smem(kMaxGroups), done);
-  if (e != cudaSuccess) return e;
-  const int ctas = n > kGroupOneCta ? kGroupCluster : 1;
-  return launch_k(group_rows_kernel, dim3(ctas), dim3(kGroupThreads), group_rows_smem(groups), st,
-                  pdl, ctas, ids, n, groups, ctas, offsets, rows, pos);
+  return groups <= kGroupWords
+             ? launch_group_rows_as<true>(ids, n, groups, offsets, rows, pos, st, pdl)
+             : launch_group_rows_as<false>(ids, n, groups, offsets, rows, pos, st, pdl);
 }
 
-template <bool BF16, bool SMALL>
-cudaError_t launch_dispatch(const void* X, int M, int K, const int* ids, int top_k, int groups,
-                            int8_t* Xq, float* s_x, int* offsets, int* rows, int* pos,
-                            cudaStream_t st, bool pdl) {
+template <bool BF16, bool SMALL, int THREADS, int REGS>
+cudaError_t launch_dispatch_as(const void* X, int M, int K, const int* ids, int top_k, int groups,
+                               int8_t* Xq, float* s_x, int* offsets, int* rows, int* pos,
+                               cudaStream_t st, bool pdl) {
   static std::atomic<bool> done[kMaxDevices];
-  const cudaError_t e = ensure_smem(dispatch_kernel<BF16, SMALL>, 65536, done);
+  const cudaError_t e = ensure_smem(dispatch_kernel<BF16, SMALL, THREADS, REGS>, 65536, done);
   if (e != cudaSuccess) return e;
-  return launch_k(dispatch_kernel<BF16, SMALL>, dim3(SMALL ? M + 1 : M), dim3(kDispatchThreads),
-                  (size_t)K, st, pdl, 1, X, M, K, ids, top_k, groups, Xq, s_x, offsets, rows, pos);
+  return launch_k(dispatch_kernel<BF16, SMALL, THREADS, REGS>, dim3(SMALL ? M + 1 : M),
+                  dim3(THREADS), (size_t)K, st, pdl, 1, X, M, K, ids, top_k, groups, Xq, s_x,
+                  offsets, rows, pos);
+}
+
+// 16 bytes a vector: 4 fp32 or 8 bf16
+template <bool BF16, bool SMALL, typename... Args>
+cudaError_t launch_dispatch(const void* X, int M, int K, Args... rest) {
+  constexpr int H = BF16 ? 1 : 2;
+  if (K <= 1024) return launch_dispatch_as<BF16, SMALL, 128, H>(X, M, K, rest...);
+  if (K <= 2048) return launch_dispatch_as<BF16, SMALL, 256, H>(X, M, K, rest...);
+  if (K <= 4096) return launch_dispatch_as<BF16, SMALL, 256, 2 * H>(X, M, K, rest...);
+  return launch_dispatch_as<BF16, SMALL, 256, 4 * H>(X, M, K, rest...);
 }
 
 template <typename OutT, int VEC>
@@ -1318,7 +1342,7 @@ int w4a8_moe_dispatch(const void* X, int x_type, int M, int K, const int32_t* id
                                             pos, st, pdl);
     return e == cudaSuccess ? W4A8_OK : W4A8_ERR_CUDA;
   }
-  e = launch_group_rows(ids, M * top_k, experts, offsets, rows, pos, st, pdl);
+  e = launch_group_rows(ids, M * top_k, experts, offsets, nullptr, pos, st, pdl);
   if (e != cudaSuccess) return W4A8_ERR_CUDA;
   if (M == 0) return W4A8_OK;
   // (the second kernel may start early whatever the flags: it reads only X
