@@ -448,6 +448,13 @@ def w4a8_gemm_fused(X, packed, out=None, stream=None, flags=0):
     return Y
 
 
+# (The helpers below keep a call's own cost down: the bare device number and
+# stream handle instead of the objects torch.cuda makes of them, which took
+# 5 of the 12 us of a small call, and one look at each property.)
+_device_now = _torch._C._cuda_getDevice if hasattr(_torch._C, "_cuda_getDevice") else None
+_stream_now = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _typed(t, ndim, name):
     """The element type code of a contiguous fp32 or bf16 CUDA tensor."""
     if not isinstance(t, _torch.Tensor) or not t.is_cuda:
@@ -460,31 +467,24 @@ def _typed(t, ndim, name):
 
 def _together(stream, first, *others):
     """All tensors on one device, which has to be the current one (the
-    kernels are launched there), and the stream's handle.  The current stream
-    is asked for its bare handle: making a Stream object of it takes 3 us,
-    a third of a small call."""
+    kernels are launched there), and the stream's handle."""
     d = first.get_device()
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("tensors on %s and %s" % (first.device, t.device))
-    if d != _torch.cuda.current_device():
-        raise ValueError("tensors on %s, but the current device is cuda:%d"
-                         % (first.device, _torch.cuda.current_device()))
+    if d != (_device_now() if _device_now else _torch.cuda.current_device()):
+        raise ValueError("tensors on %s, which is not the current device" % first.device)
     if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(d)
+        return _stream_now(d) if _stream_now else _torch.cuda.current_stream().cuda_stream
     if stream.device.index != d:
         raise ValueError("tensors on %s, stream on %s" % (first.device, stream.device))
     return stream.cuda_stream
 
 
-def _is(t, dtype, shape, d):
-    """Whether t is a contiguous tensor of this type and shape on CUDA device d."""
-    return (isinstance(t, _torch.Tensor) and t.dtype == dtype and t.shape == shape
-            and t.get_device() == d and t.is_contiguous())
-
-
 def _need_out(t, dtype, shape, d, name):
-    if not _is(t, dtype, shape, d):
+    """The caller's output buffer on CUDA device d, checked as _out does."""
+    if (not isinstance(t, _torch.Tensor) or t.dtype != dtype or t.shape != shape
+            or t.get_device() != d or not t.is_contiguous()):
         raise TypeError("%s must be a contiguous %s tensor of shape %s on cuda:%d" %
                         (name, dtype, tuple(shape), d))
 

@@ -18,8 +18,8 @@
 // gives each lane adjacent output columns.  All operands pass through one
 // ring of shared memory stages filled by 16-byte asynchronous copies.
 // Loading fragments straight from global memory, two steps ahead in
-// registers, measured 154 us where the ring takes 114 (8192 rows, K = N =
-// 8192, rank 32, fp32 x: 549 MB, 4.8 TB/s); asking A and B into L2 first
+// registers, measured 154 us where the ring takes 110 (8192 rows, K = N =
+// 8192, rank 32, fp32 x: 549 MB, 5.0 TB/s); asking A and B into L2 first
 // made a decode batch slower (28 us against 25).
 //
 // Rounding: fp32 activations and t enter the MMAs as two bf16 terms (the
@@ -81,20 +81,27 @@ struct LoraCfg {
   static constexpr int kWarpsN = WR == 1 ? 2 : 1;
   static constexpr int kWarpsK = kLoraWarps / (WR * kWarpsN);
   static constexpr int kTileRows = 16 * WR;
-  // shared memory: a ring of stages, each WK blocks of 32 k of x and A, or
-  // WK slices of 32 columns of Y and B; then the sums of t
-  static constexpr int kXBytes = kTileRows * kWarpsK * (BF16X ? 64 : 128);
-  static constexpr int kABytes = NT * 8 * kWarpsK * 64;
+  // Shared memory: a ring of stages, each kBlocksK blocks of 32 k of x and A,
+  // or kSlices slices of 32 columns of Y and B; then the sums of t.  A warp
+  // of a tall tile takes two of 64 bytes a row at a time where the ring has
+  // room (113 -> 110 us for the case above, 40 -> 38 for its first product
+  // with bf16 x).
+  static constexpr int kBlocksK = kWarpsK * (WR > 1 && NT <= 4 && BF16X ? 2 : 1);
+  static constexpr int kSlices = kWarpsK * (WR > 1 && NT <= 4 ? 2 : 1);
+  static constexpr int max2(int a, int b) { return a > b ? a : b; }
+  static constexpr int kXBytes =
+      kTileRows * max2(kBlocksK * (BF16X ? 64 : 128), kSlices * 64);
+  static constexpr int kABytes = NT * 8 * 64 * max2(kBlocksK, kSlices);
   static constexpr int kStageBytes = kXBytes + kABytes;
   static constexpr int kPitch = NT * 8 + 4;  // floats per row of t
   static constexpr int kPartFloats = kTileRows * kPitch;
   static constexpr int kParts = kWarpsK / 2;
   static constexpr bool kInPlace = kParts == 1;
   static constexpr int kSumBytes = (kParts + !kInPlace) * kPartFloats * 4;
-  // two CTAs an SM where each has three stages, and up to six stages each
+  // two CTAs an SM where each has three stages, and up to eight stages each
   static constexpr int fit(int ctas) { return (228 * 1024 / ctas - 2600 - kSumBytes) / kStageBytes; }
   static constexpr int kResident = fit(2) >= 3 ? 2 : 1;
-  static constexpr int kStages = fit(kResident) > 6 ? 6 : fit(kResident);
+  static constexpr int kStages = fit(kResident) > 8 ? 8 : fit(kResident);
   static constexpr int kSmemBytes = kStages * kStageBytes + kSumBytes;
   static_assert(kStages >= 3, "ring");
 };
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraCfg<BF16X, NT, WR>::kResiden
 lora_kernel(const LoraParams p) {
   using C = LoraCfg<BF16X, NT, WR>;
   constexpr int TM = C::kTileRows, WK = C::kWarpsK, WN = C::kWarpsN, RP = C::kPitch;
-  constexpr int S = C::kStages;
+  constexpr int S = C::kStages, BK = C::kBlocksK, BS = C::kSlices;
   extern __shared__ __align__(128) uint8_t lsm[];
   float* part = reinterpret_cast<float*>(lsm + S * C::kStageBytes);  // [kParts][TM][RP]
   float* full = part + (C::kInPlace ? 0 : C::kParts) * C::kPartFloats;  // [TM][RP]
@@ -216,8 +223,7 @@ lora_kernel(const LoraParams p) {
   // this lane's two rows of the warp's 16
   const int tok[2] = {toks[wr * 16 + g], toks[wr * 16 + g + 8]};
 
-  // this CTA's stretches of K (blocks of 32) and of N (slices of 32), WK of
-  // them a stage
+  // this CTA's stretches of K (blocks of 32) and of N (slices of 32)
   const int nkb = p.K / 32;
   const int kb0 = (int)((long long)nkb * rank_c / p.ctas);
   const int kb1 = (int)((long long)nkb * (rank_c + 1) / p.ctas);
@@ -225,7 +231,7 @@ lora_kernel(const LoraParams p) {
   const int parts = p.ctas * gridDim.y, my = blockIdx.y * p.ctas + rank_c;
   const int s0 = (int)((long long)slices * my / parts);
   const int s1 = (int)((long long)slices * (my + 1) / parts);
-  const int n_a = (kb1 - kb0 + WK - 1) / WK, n_b = (s1 - s0 + WK - 1) / WK;
+  const int n_a = (kb1 - kb0 + BK - 1) / BK, n_b = (s1 - s0 + BS - 1) / BS;  // stages
   const uint16_t* A = p.A + (size_t)adapter * p.rank * p.K;
   const uint16_t* B = p.B + (size_t)adapter * p.N * p.rank;
 
@@ -238,72 +244,76 @@ lora_kernel(const LoraParams p) {
   // In tall tiles the rows past the tile's last copy its first, unread.
   // What a thread copies keeps its place from stage to stage, so the
   // addresses are found once and advance by a constant.
-  constexpr int XC = WK * (BF16X ? 4 : 8), HC = WK * 4;  // chunks of a row: x; A and Y
-  constexpr int XS = kLoraThreads / XC, HS = kLoraThreads / HC;  // rows apart
-  constexpr int XI = TM / XS, YI = TM / HS;
-  static_assert(XI * XS == TM && YI * HS == TM && XS % 2 == 0 && HS % 2 == 0, "copies");
-  const int xrow = tid / XC, xch = tid % XC, hrow = tid / HC, hch = tid % HC;
+  constexpr int XC = BK * (BF16X ? 4 : 8), AC = BK * 4, YC = BS * 4;  // chunks of a row
+  constexpr int XS = kLoraThreads / XC, AS = kLoraThreads / AC, YS = kLoraThreads / YC;  // rows apart
+  constexpr int XI = TM / XS, YI = TM / YS, RI = XI > YI ? XI : YI;
+  static_assert(XI * XS == TM && YI * YS == TM && XS % 2 == 0 && AS % 2 == 0 && YS % 2 == 0,
+                "copies");
+  const int xrow = tid / XC, xch = tid % XC, arow = tid / AC, ach = tid % AC;
+  const int yrow0 = tid / YC, ych = tid % YC;
   const uint32_t xto = (xrow * XC + (BF16X ? xch ^ ((xrow & 1) * 4) : xch ^ (xrow & 1))) * 16;
-  const uint32_t hto = (hrow * HC + (hch ^ ((hrow & 1) * 4))) * 16;
+  const uint32_t ato = (arow * AC + (ach ^ ((arow & 1) * 4))) * 16;
+  const uint32_t yto = (yrow0 * YC + (ych ^ ((yrow0 & 1) * 4))) * 16;
   const int rc = p.rank / 8;  // chunks of a column of B
   const int flip = rc == 8 ? 3 : rc == 16 ? 4 : 31;  // the bit of a chunk's index that tells odd columns
-  const uint8_t* xp[XI];
-  const uint8_t* yq[YI];
-  unsigned xin = 0, yin = 0;
-#pragma unroll
-  for (int i = 0; i < XI; ++i) {
-    int m = toks[xrow + i * XS];
+  const uint8_t* rp[RI];  // this thread's chunks of x, then of Y
+  unsigned rin = 0;
+  auto row_of = [&](int i, int r) {
+    int m = toks[r];
     if (WR > 1 && m < 0) m = toks[0];
-    if (m >= 0) xin |= 1u << i;
-    xp[i] = static_cast<const uint8_t*>(p.X) +
-            ((size_t)max(m, 0) * p.ldx + 32 * kb0) * (BF16X ? 2 : 4) + xch * 16;
-  }
+    if (m >= 0) rin |= 1u << i;
+    return (size_t)max(m, 0);
+  };
 #pragma unroll
-  for (int i = 0; i < YI; ++i) {
-    int m = toks[hrow + i * HS];
-    if (WR > 1 && m < 0) m = toks[0];
-    if (m >= 0 && p.y_vec) yin |= 1u << i;
-    yq[i] = reinterpret_cast<const uint8_t*>(p.Y + (size_t)max(m, 0) * p.ldy + 32 * s0) + hch * 16;
-  }
-  const uint8_t* ap = reinterpret_cast<const uint8_t*>(A + (size_t)hrow * p.K + 32 * kb0) + hch * 16;
+  for (int i = 0; i < XI; ++i)
+    rp[i] = static_cast<const uint8_t*>(p.X) +
+            (row_of(i, xrow + i * XS) * p.ldx + 32 * kb0) * (BF16X ? 2 : 4) + xch * 16;
+  const uint8_t* ap = reinterpret_cast<const uint8_t*>(A + (size_t)arow * p.K + 32 * kb0) + ach * 16;
   const uint8_t* bp = reinterpret_cast<const uint8_t*>(B + (size_t)32 * s0 * p.rank) + tid * 16;
   int ahead = 0;          // the next stage to copy,
   uint32_t st_in = ring;  // and where it goes
   auto issue = [&]() {
     if (ahead < n_a) {
-      const int left = kb1 - kb0 - ahead * WK;  // blocks
+      const int left = kb1 - kb0 - ahead * BK;  // blocks
       if (xch < left * (BF16X ? 4 : 8)) {
 #pragma unroll
         for (int i = 0; i < XI; ++i)
-          if (WR > 1 || (xin >> i & 1)) cp_async16(st_in + xto + i * 4096, xp[i]);
+          if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + xto + i * 4096, rp[i]);
       }
 #pragma unroll
-      for (int i = 0; i < XI; ++i) xp[i] += XC * 16;
-      if (hch < left * 4) {
+      for (int i = 0; i < XI; ++i) rp[i] += XC * 16;
+      if (ach < left * 4) {
 #pragma unroll
-        for (int i = 0; i < (NT * 8 + HS - 1) / HS; ++i)
-          if (hrow + i * HS < p.rank)
-            cp_async16(st_in + C::kXBytes + hto + i * 4096, ap + (size_t)i * HS * p.K * 2);
+        for (int i = 0; i < (NT * 8 + AS - 1) / AS; ++i)
+          if (arow + i * AS < p.rank)
+            cp_async16(st_in + C::kXBytes + ato + i * 4096, ap + (size_t)i * AS * p.K * 2);
       }
-      ap += HC * 16;
+      ap += AC * 16;
     } else if (ahead < n_a + n_b) {
-      const int n = (s0 + (ahead - n_a) * WK) * 32;
-      const int cols = min(min(WK * 32, s1 * 32 - n), p.N - n);
-      if (hch * 8 + 8 <= cols && p.y_vec) {
+      if (ahead == n_a) {
+        rin = 0;
 #pragma unroll
         for (int i = 0; i < YI; ++i)
-          if (WR > 1 || (yin >> i & 1)) cp_async16(st_in + hto + i * 4096, yq[i]);
+          rp[i] = reinterpret_cast<const uint8_t*>(p.Y + row_of(i, yrow0 + i * YS) * p.ldy + 32 * s0) +
+                  ych * 16;
+      }
+      const int n = (s0 + (ahead - n_a) * BS) * 32;
+      const int cols = min(min(BS * 32, s1 * 32 - n), p.N - n);
+      if (ych * 8 + 8 <= cols && p.y_vec) {
+#pragma unroll
+        for (int i = 0; i < YI; ++i)
+          if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + yto + i * 4096, rp[i]);
       }
 #pragma unroll
-      for (int i = 0; i < YI; ++i) yq[i] += HC * 16;
+      for (int i = 0; i < YI; ++i) rp[i] += YC * 16;
       const int chunks = cols * rc;
 #pragma unroll
-      for (int i = 0; i < (WK * 32 * NT + kLoraThreads - 1) / kLoraThreads; ++i) {
+      for (int i = 0; i < (BS * 32 * NT + kLoraThreads - 1) / kLoraThreads; ++i) {
         const int at = tid + i * kLoraThreads;
         if (at < chunks)
           cp_async16(st_in + C::kXBytes + (at ^ ((at >> flip & 1) * 4)) * 16, bp + i * 4096);
       }
-      bp += WK * 64 * p.rank;
+      bp += BS * 64 * p.rank;
     }
     cp_async_commit();
     ++ahead;
@@ -327,8 +337,7 @@ lora_kernel(const LoraParams p) {
   const int nt = p.rank / 8 - wn * NW;
   const uint32_t x_at = (wr * 16 + g) * XC * 16 +
                         (BF16X ? (wk * 4 + c) ^ (odd * 4) : wk * 8 + 2 * c + odd) * 16;
-  const uint32_t h_at = ((wk * 4 + c) ^ (odd * 4)) * 16;
-  const uint32_t a_at = C::kXBytes + (wn * NW * 8 + g) * HC * 16 + h_at;
+  const uint32_t a_at = C::kXBytes + (wn * NW * 8 + g) * AC * 16 + ((wk * 4 + c) ^ (odd * 4)) * 16;
   uint32_t st = ring;
   auto next = [&]() {
     cp_async_wait<S - 2>();
@@ -340,14 +349,17 @@ lora_kernel(const LoraParams p) {
     if (st == ring + S * C::kStageBytes) st = ring;
   };
 #pragma unroll 1
-  for (int kb = kb0 + wk; kb < kb0 + wk + n_a * WK; kb += WK) {
+  for (int kb = kb0 + wk; kb < kb0 + wk + n_a * BK; kb += BK) {
     next();
-    if (kb < kb1) {
+#pragma unroll
+    for (int u = 0; u < BK / WK; ++u) {  // (WK blocks apart: the parity of 4 chunks is kept)
+      if (kb + u * WK >= kb1) continue;
+      const uint32_t xs = st + x_at + u * WK * (BF16X ? 64 : 128), as = st + a_at + u * WK * 64;
       // hi and lo words: [row half][k pair]
       uint32_t hi[2][4], lo[2][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t x = st + x_at + h * 8 * XC * 16;
+        const uint32_t x = xs + h * 8 * XC * 16;
         const uint4 u = lds128(x);
         if constexpr (BF16X) {
           hi[h][0] = u.x;
@@ -369,7 +381,7 @@ lora_kernel(const LoraParams p) {
         if (j0 >= nt) continue;
         uint4 w[JB];
 #pragma unroll
-        for (int j = 0; j < JB; ++j) w[j] = lds128(st + a_at + (j0 + j) * 8 * HC * 16);
+        for (int j = 0; j < JB; ++j) w[j] = lds128(as + (j0 + j) * 8 * AC * 16);
 #pragma unroll
         for (int j = 0; j < JB; ++j)
           mma_bf16(acc[j0 + j], hi[0][0], hi[1][0], hi[0][1], hi[1][1], w[j].x, w[j].y);
@@ -475,7 +487,7 @@ lora_kernel(const LoraParams p) {
   constexpr int QN = 4 / WN, CW = 2 * QN, YW = QN;  // YW: words of a row of Y
   const int jcol = wn * 16 + (g >> 1) * CW + odd;   // + 2 q: the column of MMA column g, tile q
   const int ycol = wn * 16 + CW * c;                // this lane's first column
-  const uint32_t y_at = (wr * 16 + g) * HC * 16 +
+  const uint32_t y_at = (wr * 16 + g) * YC * 16 +
                         ((wk * 4 + ycol / 8) ^ (odd * 4)) * 16 + (ycol % 8) * 2;
   const int b_at = (wk * 32 + jcol) * rc;           // chunk
   // (a lane past p.rank, where t is zero, reads its column's first chunk)
@@ -490,16 +502,19 @@ lora_kernel(const LoraParams p) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) yrow[h] = p.Y + (size_t)max(tok[h], 0) * p.ldy;
 #pragma unroll 1
-  for (int sl = s0 + wk; sl < s0 + wk + n_b * WK; sl += WK) {
+  for (int s_at = s0 + wk; s_at < s0 + wk + n_b * BS; s_at += BS) {
     next();
-    if (sl < s1) {
+#pragma unroll
+    for (int u = 0; u < BS / WK; ++u) {
+      const int sl = s_at + u * WK;
+      if (sl >= s1) continue;
       const int col = sl * 32 + ycol;
       const bool whole = p.y_vec && (col & ~7) + 8 <= p.N;
       float d[QN][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[YW];
-        const uint32_t at = st + y_at + h * 8 * HC * 16;
+        const uint32_t at = st + y_at + u * WK * 64 + h * 8 * YC * 16;
         if constexpr (YW == 4) {
           const uint4 v = lds128(at);
           w[0] = v.x;
@@ -530,7 +545,8 @@ lora_kernel(const LoraParams p) {
       for (int b = 0; b < NB; ++b) {
         uint32_t w[QN][KW / 2];
         // (the columns' parity, and so the exchange of halves, is the lane's)
-        const uint32_t ad = st + C::kXBytes + ((b_at + b_ch[b]) ^ b_flip) * 16 + b_sub;
+        const uint32_t ad =
+            st + C::kXBytes + ((b_at + u * WK * 32 * rc + b_ch[b]) ^ b_flip) * 16 + b_sub;
 #pragma unroll
         for (int q = 0; q < QN; ++q) {
           if constexpr (KW == 8) {

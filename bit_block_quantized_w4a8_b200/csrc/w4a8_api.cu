@@ -1028,19 +1028,24 @@ cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream
   return launch_lora_as<BF16X, 16, WR>(p, slots, parts, st, pdl);
 }
 
-// Row tiles of 64 where adapters have 32 rows or more on average, else of 16;
-// a tile's cluster, then the further split of N, grow while the CTAs still
-// fit the machine at once, two an SM (one more doubling is a second wave:
-// 32 rows of 32 adapters, K = 8192, N = 10240, rank 64, take 20 us with 256
-// CTAs, 30 with 512, 35 with 64), a CTA keeping 256 k and 128 columns.
+// Row tiles of 64 where adapters have 32 rows or more on average and there
+// are tiles enough to fill the machine (8192 rows, 8192 x 8192, rank 32: 111 us
+// against 144 with tiles of 16; 1024 rows, 4096 x 4096, bf16: 21 against 16),
+// else of 16.  A tile's cluster grows while the CTAs still fit the machine
+// at once, two an SM (one more doubling is a second wave: 32 rows of 32
+// adapters, 8192 x 10240, rank 64, take 20 us with 256 CTAs, 30 with 512, 35
+// with 64), a CTA keeping 256 k.  With few tiles N is split further, which
+// repeats the first product: one row, 4096 x 12288: 8.1 us with 64 CTAs, 9.4
+// with 16, 11.2 with 8; but 8 tiles are best left at 64 CTAs (9.4 against
+// 10.8 with 256).
 cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool pdl) {
   const int used = p.adapters < p.M ? p.adapters : p.M;
-  const bool tall = p.M / used >= 32;
+  const bool tall = p.M / used >= 32 && p.M / 64 >= sms / 3;
   const int tm = tall ? 64 : 16;
   const int slots = (int)(((long long)p.M + (long long)used * (tm - 1)) / tm);
   int ctas = 1, parts = 1;
   while (ctas < 8 && (long long)slots * ctas * 2 <= 2 * sms && p.K >= 512 * ctas) ctas *= 2;
-  while ((long long)slots * ctas * parts * 2 <= 2 * sms && p.N >= 256 * ctas * parts) parts *= 2;
+  while (slots * ctas * parts * 4 <= sms && p.N >= 256 * ctas * parts) parts *= 2;
   p.ctas = ctas;
   if (tall)
     return bf16x ? launch_lora_nt<true, 4>(p, slots, parts, st, pdl)

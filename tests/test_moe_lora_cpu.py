@@ -115,7 +115,7 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
         def __init__(self, index):
             self.device = torch.device("cuda", index)
             self.get_device = lambda: index
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(w4, "_device_now", lambda: 0)
     with pytest.raises(ValueError, match="and cuda:1"):
         w4._together(None, T(0), T(1))
     with pytest.raises(ValueError, match="current device"):
