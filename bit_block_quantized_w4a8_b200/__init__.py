@@ -659,30 +659,33 @@ def w4a8_lora(X, Y, A, B, ids, scale=None, stream=None, flags=0):
     for t, name in ((X, "X"), (Y, "Y")):
         if not isinstance(t, _torch.Tensor) or not t.is_cuda:
             raise TypeError("%s must be a CUDA tensor" % name)
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise TypeError("%s must be 2D with adjacent columns" % name)
+        if t.dim() != 2:
+            raise TypeError("%s must be 2D" % name)
     kind = _TYPES.get(X.dtype)
     if kind is None or Y.dtype != _torch.bfloat16:
         raise TypeError("X must be float32 or bfloat16 and Y bfloat16")
+    (M, K), (ldx, x1), (M2, N), (ldy, y1) = X.shape, X.stride(), Y.shape, Y.stride()
+    if (x1 != 1 and K > 1) or (y1 != 1 and N > 1):
+        raise TypeError("X and Y must have adjacent columns")
+    if M <= 1:  # (a single row's stride says nothing)
+        ldx, ldy = max(ldx, K), max(ldy, N)
     _need(A, _torch.bfloat16, 3, "A")
     _need(B, _torch.bfloat16, 3, "B")
-    M, K = X.shape
-    N = Y.shape[1]
-    L, r = A.shape[:2]
-    if Y.shape[0] != M or A.shape[2] != K or tuple(B.shape) != (L, N, r):
+    L, r, K2 = A.shape
+    if M2 != M or K2 != K or B.shape != (L, N, r):
         raise ValueError("shape mismatch: X %s, Y %s, A %s, B %s" % (
             tuple(X.shape), tuple(Y.shape), tuple(A.shape), tuple(B.shape)))
     if scale is not None:
         _need(scale, _torch.float32, 1, "scale")
         if scale.numel() != L:
             raise ValueError("scale has %d entries for %d adapters" % (scale.numel(), L))
-    plan = None
+    offsets = rows = None
     if isinstance(ids, LoraPlan):
-        plan, ids = ids, None
-        if plan.M != M or plan.adapters != L:
+        if ids.M != M or ids.adapters != L:
             raise ValueError("the plan is for %d rows and %d adapters, not %d and %d"
-                             % (plan.M, plan.adapters, M, L))
-        st = _together(stream, X, Y, A, B, scale, plan.rows, plan.offsets)
+                             % (ids.M, ids.adapters, M, L))
+        offsets, rows, ids = ids.offsets, ids.rows, None
+        st = _together(stream, X, Y, A, B, scale, rows, offsets)
     else:
         _need(ids, _torch.int32, 1, "ids")
         if ids.numel() != M:
@@ -691,14 +694,13 @@ def w4a8_lora(X, Y, A, B, ids, scale=None, stream=None, flags=0):
         if M > LORA_IDS_MAX:
             # (the second kernel may start early: it waits before it reads)
             plan, ids = w4a8_lora_plan(ids, L, stream=stream, flags=flags), None
+            offsets, rows = plan.offsets, plan.rows
             flags |= W4A8_FLAG_PDL
-    ldx = X.stride(0) if M > 1 else max(X.stride(0), K)
-    ldy = Y.stride(0) if M > 1 else max(Y.stride(0), N)
     rc = lib().w4a8_lora(X.data_ptr(), kind, ldx, M, K, A.data_ptr(), B.data_ptr(), r, L,
                          None if scale is None else scale.data_ptr(),
                          None if ids is None else ids.data_ptr(),
-                         None if plan is None else plan.offsets.data_ptr(),
-                         None if plan is None else plan.rows.data_ptr(), N, Y.data_ptr(), ldy,
+                         None if offsets is None else offsets.data_ptr(),
+                         None if rows is None else rows.data_ptr(), N, Y.data_ptr(), ldy,
                          flags, st)
     if rc:
         _check(rc, "w4a8_lora")
