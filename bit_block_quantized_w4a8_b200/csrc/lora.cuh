@@ -36,11 +36,9 @@
 
 namespace w4a8 {
 
-constexpr int kLoraThreads = 256;
-constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = kMaxGroups;
-constexpr int kLoraIdsMax = kLoraThreads;  // rows that a CTA groups by itself
+constexpr int kLoraIdsMax = 256;  // rows that a CTA groups by itself, one a thread
 
 struct LoraParams {
   const void* X;
@@ -73,13 +71,14 @@ __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uin
   lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
 }
 
-// The eight warps of a CTA: WR row groups of 16, WK blocks of 32 k (slices of
-// 32 columns in the second product), WN parts of the rank tiles (of a slice's
+// The warps of a CTA: WR row groups of 16, WK blocks of 32 k (slices of 32
+// columns in the second product), WN parts of the rank tiles (of a slice's
 // columns).
 template <bool BF16X, int NT, int WR>
 struct LoraCfg {
+  static constexpr int kThreads = 256;
   static constexpr int kWarpsN = WR == 1 ? 2 : 1;
-  static constexpr int kWarpsK = kLoraWarps / (WR * kWarpsN);
+  static constexpr int kWarpsK = kThreads / 32 / (WR * kWarpsN);
   static constexpr int kTileRows = 16 * WR;
   // Shared memory: a ring of stages, each kBlocksK blocks of 32 k of x and A,
   // or kSlices slices of 32 columns of Y and B; then the sums of t.  A warp
@@ -124,13 +123,55 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
+// The slot-th tile that holds rows of a plan, counting adapter by adapter:
+// its adapter (-1: there are not so many), its rows in toks (-1 past the
+// last) and their number.  Every thread of the CTA calls it.
+template <int TM>
+__device__ __forceinline__ int lora_tile(const LoraParams& p, int slot, int tid, int* toks,
+                                         int& cnt) {
+  const int lane = tid & 31;
+  int adapter = -1, seen = 0, r0 = 0;
+  for (int a0 = 0; a0 < p.adapters && adapter < 0; a0 += 32) {
+    const int a = a0 + lane;
+    int o0 = 0, o1 = 0;
+    if (a < p.adapters) {
+      o0 = p.offsets[a];
+      o1 = p.offsets[a + 1];
+      if (o0 < 0 || o1 < o0 || o1 > p.M) o1 = o0 = 0;
+    }
+    const int t = (o1 - o0 + TM - 1) / TM;
+    int incl = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, seen + incl > slot);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      adapter = a0 + src;
+      const int first = __shfl_sync(0xffffffffu, seen + incl - t, src);
+      r0 = __shfl_sync(0xffffffffu, o0, src) + (slot - first) * TM;
+      cnt = min(TM, __shfl_sync(0xffffffffu, o1, src) - r0);
+    }
+    seen += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (adapter < 0) return -1;
+  if (tid < TM) {
+    const int m = tid < cnt ? p.rows[r0 + tid] : -1;
+    toks[tid] = (unsigned)m < (unsigned)p.M ? m : -1;
+  }
+  __syncthreads();
+  return adapter;
+}
+
 // NT: tiles of 8 ranks (ranks past p.rank are zero); WR: tiles of 16 rows.
 template <bool BF16X, int NT, int WR>
-__global__ void __launch_bounds__(kLoraThreads, LoraCfg<BF16X, NT, WR>::kResident)
+__global__ void __launch_bounds__(LoraCfg<BF16X, NT, WR>::kThreads, LoraCfg<BF16X, NT, WR>::kResident)
 lora_kernel(const LoraParams p) {
   using C = LoraCfg<BF16X, NT, WR>;
   constexpr int TM = C::kTileRows, WK = C::kWarpsK, WN = C::kWarpsN, RP = C::kPitch;
-  constexpr int S = C::kStages, BK = C::kBlocksK, BS = C::kSlices;
+  constexpr int NTHR = C::kThreads, S = C::kStages, BK = C::kBlocksK, BS = C::kSlices;
   extern __shared__ __align__(128) uint8_t lsm[];
   float* part = reinterpret_cast<float*>(lsm + S * C::kStageBytes);  // [kParts][TM][RP]
   float* full = part + (C::kInPlace ? 0 : C::kParts) * C::kPartFloats;  // [TM][RP]
@@ -146,12 +187,12 @@ lora_kernel(const LoraParams p) {
   // the slot-th tile that holds rows: its adapter, and its rows in toks
   __shared__ int toks[TM];
   int adapter = -1, cnt = 0;
-  if (p.ids != nullptr) {
+  if (WR == 1 && p.ids != nullptr) {
     // few rows (one per thread), not grouped yet: a row that has a multiple
     // of TM rows of its adapter before it opens a tile, and tiles count in
     // the order of the rows that open them
     __shared__ __align__(16) int sid[kLoraIdsMax];
-    __shared__ int opens[kLoraWarps];
+    __shared__ int opens[NTHR / 32];
     __shared__ int found[3];  // adapter, first rank, rows
     int id = tid < p.M ? p.ids[tid] : -1;
     if ((unsigned)id >= (unsigned)p.adapters) id = -1;
@@ -186,38 +227,8 @@ lora_kernel(const LoraParams p) {
     __syncthreads();
     cnt = found[2];
   } else {
-    int seen = 0, r0 = 0;
-    for (int a0 = 0; a0 < p.adapters && adapter < 0; a0 += 32) {
-      const int a = a0 + lane;
-      int o0 = 0, o1 = 0;
-      if (a < p.adapters) {
-        o0 = p.offsets[a];
-        o1 = p.offsets[a + 1];
-        if (o0 < 0 || o1 < o0 || o1 > p.M) o1 = o0 = 0;
-      }
-      const int t = (o1 - o0 + TM - 1) / TM;
-      int incl = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, seen + incl > slot);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        adapter = a0 + src;
-        const int first = __shfl_sync(0xffffffffu, seen + incl - t, src);
-        r0 = __shfl_sync(0xffffffffu, o0, src) + (slot - first) * TM;
-        cnt = min(TM, __shfl_sync(0xffffffffu, o1, src) - r0);
-      }
-      seen += __shfl_sync(0xffffffffu, incl, 31);
-    }
+    adapter = lora_tile<TM>(p, slot, tid, toks, cnt);
     if (adapter < 0) return;  // the whole cluster: a slot past the last tile
-    if (tid < TM) {
-      const int m = tid < cnt ? p.rows[r0 + tid] : -1;
-      toks[tid] = (unsigned)m < (unsigned)p.M ? m : -1;
-    }
-    __syncthreads();
   }
 
   // this lane's two rows of the warp's 16
@@ -245,7 +256,7 @@ lora_kernel(const LoraParams p) {
   // What a thread copies keeps its place from stage to stage, so the
   // addresses are found once and advance by a constant.
   constexpr int XC = BK * (BF16X ? 4 : 8), AC = BK * 4, YC = BS * 4;  // chunks of a row
-  constexpr int XS = kLoraThreads / XC, AS = kLoraThreads / AC, YS = kLoraThreads / YC;  // rows apart
+  constexpr int XS = NTHR / XC, AS = NTHR / AC, YS = NTHR / YC;  // rows apart
   constexpr int XI = TM / XS, YI = TM / YS, RI = XI > YI ? XI : YI;
   static_assert(XI * XS == TM && YI * YS == TM && XS % 2 == 0 && AS % 2 == 0 && YS % 2 == 0,
                 "copies");
@@ -278,7 +289,7 @@ lora_kernel(const LoraParams p) {
       if (xch < left * (BF16X ? 4 : 8)) {
 #pragma unroll
         for (int i = 0; i < XI; ++i)
-          if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + xto + i * 4096, rp[i]);
+          if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + xto + i * NTHR * 16, rp[i]);
       }
 #pragma unroll
       for (int i = 0; i < XI; ++i) rp[i] += XC * 16;
@@ -286,7 +297,7 @@ lora_kernel(const LoraParams p) {
 #pragma unroll
         for (int i = 0; i < (NT * 8 + AS - 1) / AS; ++i)
           if (arow + i * AS < p.rank)
-            cp_async16(st_in + C::kXBytes + ato + i * 4096, ap + (size_t)i * AS * p.K * 2);
+            cp_async16(st_in + C::kXBytes + ato + i * NTHR * 16, ap + (size_t)i * AS * p.K * 2);
       }
       ap += AC * 16;
     } else if (ahead < n_a + n_b) {
@@ -302,16 +313,16 @@ lora_kernel(const LoraParams p) {
       if (ych * 8 + 8 <= cols && p.y_vec) {
 #pragma unroll
         for (int i = 0; i < YI; ++i)
-          if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + yto + i * 4096, rp[i]);
+          if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + yto + i * NTHR * 16, rp[i]);
       }
 #pragma unroll
       for (int i = 0; i < YI; ++i) rp[i] += YC * 16;
       const int chunks = cols * rc;
 #pragma unroll
-      for (int i = 0; i < (BS * 32 * NT + kLoraThreads - 1) / kLoraThreads; ++i) {
-        const int at = tid + i * kLoraThreads;
+      for (int i = 0; i < (BS * 32 * NT + NTHR - 1) / NTHR; ++i) {
+        const int at = tid + i * NTHR;
         if (at < chunks)
-          cp_async16(st_in + C::kXBytes + (at ^ ((at >> flip & 1) * 4)) * 16, bp + i * 4096);
+          cp_async16(st_in + C::kXBytes + (at ^ ((at >> flip & 1) * 4)) * 16, bp + i * NTHR * 16);
       }
       bp += BS * 64 * p.rank;
     }
@@ -428,7 +439,7 @@ lora_kernel(const LoraParams p) {
   }
   const float s = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
   if (p.ctas > 1 && C::kParts > 1) {
-    for (int i = tid; i < cnt * NT * 8; i += kLoraThreads) {
+    for (int i = tid; i < cnt * NT * 8; i += NTHR) {
       const int at = i / (NT * 8) * RP + i % (NT * 8);
       float v = part[at];
 #pragma unroll
@@ -439,11 +450,11 @@ lora_kernel(const LoraParams p) {
   if (p.ctas > 1) cluster_sync_all();
   // (with one part the totals take its place, so every CTA of the cluster has
   // to be done reading first)
-  constexpr int EI = TM * NT * 8 / kLoraThreads;
+  constexpr int EI = TM * NT * 8 / NTHR;
   float sum[EI];
 #pragma unroll
   for (int e = 0; e < EI; ++e) {
-    const int i = tid + e * kLoraThreads;
+    const int i = tid + e * NTHR;
     const int r = i / (NT * 8), at = r * RP + i % (NT * 8);
     sum[e] = 0.0f;
     if (r < cnt && i % (NT * 8) < p.rank) {
@@ -464,7 +475,7 @@ lora_kernel(const LoraParams p) {
   if (p.ctas > 1 && C::kInPlace) cluster_wait();
 #pragma unroll
   for (int e = 0; e < EI; ++e) {
-    const int i = tid + e * kLoraThreads;
+    const int i = tid + e * NTHR;
     full[i / (NT * 8) * RP + i % (NT * 8)] = sum[e] * s;
   }
   __syncthreads();

@@ -1,0 +1,474 @@
+// lora_tc.cuh -- the adapters of lora.cuh for many rows, with the products on
+// the fifth-generation tensor cores (tcgen05).
+//
+// Tiles of 128 rows that share an adapter; a cluster of CTAs owns a tile, each
+// CTA a stretch of K and then of N, one CTA an SM.  Four producer warps fetch
+// stages (x and Y row by row, A and B by TMA), an MMA warp issues the
+// products, sixteen worker warps do the rest, each at its own pace: per stage
+// of 64 k they carry x into tensor memory, fp32 x as two bf16 terms, for the
+// MMA t += x A^T; after the cluster's sums t goes back to tensor memory in
+// two bf16 terms; and per stage of 64 columns one half of them adds d = t B^T
+// to Y's tile in shared memory, which leaves in whole lines, while the other
+// half does the next stage.  (Rows by TMA's gather4 take some 70 cycles for
+// each 512 bytes, three times what HBM gives: 255 us for the case below.)
+//
+// Warp-level MMAs do the same work at a quarter of the rate and in an
+// instruction per 2048 products; 8192 rows, 8192 x 8192, fp32 x, rank 32, 64
+// and 128: 112, 137 and 250 us there, 115, 116 and 131 here (84, 86 and 90 at
+// the measured bandwidth), so ranks over 32 come here.  With barriers of the
+// whole CTA in place of the pipelines this form took 140, 145 and 168.
+//
+// Every wait on an mbarrier is bounded.  After a timeout (or with a wait
+// budget of 0) the CTA stores nothing more, the waits that follow give up at
+// once, every hardware barrier is still reached by all, and copies and MMAs
+// under way are waited for before tensor memory is freed.
+#pragma once
+#include <cstdint>
+#include "lora.cuh"
+#include "ptx.cuh"
+
+namespace w4a8 {
+
+constexpr int kLoraTcWorkers = 512;
+constexpr int kLoraTcProducers = 128;
+constexpr int kLoraTcThreads = kLoraTcWorkers + kLoraTcProducers + 32;  // and the MMA's warp
+constexpr int kLoraTcRows = 128;
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 x bf16 -> fp32, one CTA.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0)
+      : "memory");
+}
+// Instruction descriptor of kind::f16: bf16 A and B, both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
+  return (1u << 4)                        // D format: F32
+         | (1u << 7)                      // A: bf16
+         | (1u << 10)                     // B: bf16
+         | ((uint32_t)(N >> 3) << 17)     // N / 8
+         | ((uint32_t)(M >> 4) << 24);    // M / 16
+}
+// An arrival on `bar` (counted in it) once this thread's copies so far are here.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// R: ranks, padded (64 or 128).
+template <bool BF16X, int R>
+struct LoraTcCfg {
+  // shared memory: a ring of stages of x and A (64 k), then of Y and B (64
+  // columns) in the same place, then the sums of t
+  static constexpr int kXBytes = kLoraTcRows * 64 * (BF16X ? 2 : 4);
+  static constexpr int kYBytes = kLoraTcRows * 64 * 2;
+  static constexpr int kOpBytes = R * 128;
+  static constexpr int kStageBytes = kXBytes + kOpBytes;
+  static constexpr int kStage2Bytes = kYBytes + kOpBytes;
+  static constexpr int kPitch = R + 4;                                // floats per row of t
+  static constexpr int kSumBytes = kLoraTcRows * kPitch * 4;
+  static constexpr int kFit = (226 * 1024 - 3072 - kSumBytes) / kStageBytes;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kStages2 = kStages * kStageBytes / kStage2Bytes;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kSumBytes + 1024;  // (1024: alignment)
+  static_assert(kStages >= 3, "ring");
+};
+
+// Maps: A [L r][K], boxes of 64 k by R rows; B [L N][r], boxes of 64 ranks
+// (zeros past the last) by 64 rows; both with the 128-byte swizzle (16-byte
+// chunk c of row r of a tile at c ^ (r mod 8)), which the copies of x and Y
+// follow too.
+template <bool BF16X, int R>
+__global__ void __launch_bounds__(kLoraTcThreads, 1)
+lora_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const LoraParams p, const unsigned long long lim) {
+  using C = LoraTcCfg<BF16X, R>;
+  constexpr int S = C::kStages, S2 = C::kStages2, TM = kLoraTcRows, RP = C::kPitch, Q = R / 4;
+  constexpr int NW = kLoraTcWorkers, NP = kLoraTcProducers, kMmaWarp = (NW + NP) / 32;
+  // tensor memory columns: t's accumulators and x's terms (two slots of two
+  // halves of 16 + 16 words), then t's terms and two accumulators of 64
+  constexpr uint32_t kCols = 256;
+  constexpr uint32_t kD1 = 0, kSlots = 128, kT = 128, kD2 = 0;
+  extern __shared__ uint8_t tsm_raw[];
+  __shared__ int toks[TM];
+  // barriers: a stage of the first product is here, is done with; one of the
+  // second; x's slot is filled, is free; t is summed in tensor memory; t's
+  // terms are there; a second-product accumulator is full, is free; the end
+  __shared__ alignas(8) uint64_t b_full[S], b_free[S], b_full2[S2], b_free2[S2], b_xfull[2],
+      b_xfree[2], b_d1, b_t, b_dfull[2], b_dfree[2], b_end;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const uint32_t ring = (smem_u32(tsm_raw) + 1023u) & ~1023u;
+  const uint32_t sums = ring + S * C::kStageBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank_c = p.ctas > 1 ? (int)cluster_ctarank() : 0;
+  const int slot = blockIdx.x / p.ctas;
+  volatile int* abort = &abort_flag;
+  pdl_launch_dependents();
+  pdl_wait();  // the plan, X and Y may be written by the preceding kernel
+
+  int cnt = 0;
+  const int adapter = lora_tile<TM>(p, slot, tid, toks, cnt);
+  if (adapter < 0) return;  // the whole cluster: a slot past the last tile
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&tmem_base), kCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&b_full[s]), NP + 1);
+      mbar_init(smem_u32(&b_free[s]), 1);
+    }
+    for (int s = 0; s < S2; ++s) {
+      mbar_init(smem_u32(&b_full2[s]), NP + 1);
+      mbar_init(smem_u32(&b_free2[s]), NW / 64);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&b_xfull[i]), NW / 32);
+      mbar_init(smem_u32(&b_xfree[i]), 1);
+      mbar_init(smem_u32(&b_dfull[i]), 1);
+      mbar_init(smem_u32(&b_dfree[i]), NW / 64);
+    }
+    mbar_init(smem_u32(&b_d1), 1);
+    mbar_init(smem_u32(&b_t), NW / 32);
+    mbar_init(smem_u32(&b_end), 1);
+    fence_barrier_init();
+    abort_flag = lim == 0;  // a wait budget of 0: abort before any wait
+    if (lim == 0) record_status(kDevTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  auto wait = [&](uint64_t& bar, int phase) {
+    return warp_wait(smem_u32(&bar), phase & 1, abort, lim);
+  };
+  auto arrive = [&](uint64_t& bar) {  // once a warp, after all its lanes
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
+  };
+
+  // this CTA's stretches of K and of N, in blocks of 64: a stage each
+  const int nkb = p.K / 64, slices = (p.N + 63) / 64;
+  const int kb0 = nkb * rank_c / p.ctas, n_a = nkb * (rank_c + 1) / p.ctas - kb0;
+  const int s0 = (int)((long long)slices * rank_c / p.ctas);
+  const int n_b = (int)((long long)slices * (rank_c + 1) / p.ctas) - s0;
+  auto at_stage = [&](int t) { return ring + (t % S) * C::kStageBytes; };
+  auto at_stage2 = [&](int u) { return ring + (u % S2) * C::kStage2Bytes; };
+
+  if (warp >= NW / 32 && warp < kMmaWarp) {
+    // ------------------------------------------------------------ producers
+    // A thread copies the same chunk of every so many rows; rows past the
+    // last are row 0, unread.
+    if (p.ctas > 1) cluster_arrive();  // they have nothing to add to the cluster's sums
+    constexpr int XC = BF16X ? 8 : 16, XS = NP / XC, XI = TM / XS, YS = NP / 8, YI = TM / YS;
+    const int pt = tid - NW;
+    const int xrow = pt / XC, xch = pt % XC, yrow = pt / 8, ych = pt % 8;
+    const uint32_t xto =
+        (xch / 8) * (TM * 128) + xrow * 128 + (((xch & 7) ^ (xrow & 7)) << 4);
+    const uint32_t yto = yrow * 128 + ((ych ^ (yrow & 7)) << 4);
+    static_assert(XS % 8 == 0 && YS % 8 == 0, "a thread's rows share their place in the swizzle");
+    const uint8_t* rp[XI];
+#pragma unroll
+    for (int i = 0; i < XI; ++i)
+      rp[i] = static_cast<const uint8_t*>(p.X) + xch * 16 +
+              ((size_t)max(toks[xrow + i * XS], 0) * p.ldx + 64 * kb0) * (BF16X ? 2 : 4);
+    bool met = p.ctas == 1;
+    auto meet = [&]() {  // the cluster's two barriers around its sums
+      if (!met) {
+        cluster_wait();
+        cluster_sync_all();
+        met = true;
+      }
+    };
+    int t = 0, u = 0;
+    for (; t < n_a; ++t) {
+      const int s = t % S;
+      if (t >= S && !wait(b_free[s], t / S - 1)) break;
+      const uint32_t st = at_stage(t), full = smem_u32(&b_full[s]);
+      if (pt == 0) {
+        mbar_arrive_expect_tx(full, C::kOpBytes);
+        tma_load_2d(st + C::kXBytes, &map_a, 64 * (kb0 + t), adapter * p.rank, full);
+      }
+#pragma unroll
+      for (int i = 0; i < XI; ++i) {
+        cp_async16(st + xto + i * XS * 128, rp[i]);
+        rp[i] += BF16X ? 128 : 256;
+      }
+      cp_async_arrive(full);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < YI; ++i)
+      rp[i] = reinterpret_cast<const uint8_t*>(p.Y + (size_t)max(toks[yrow + i * YS], 0) * p.ldy +
+                                               64 * s0 + ych * 8);
+    for (bool ok = t == n_a; ok && u < n_b; ++u) {
+      const int s = u % S2;
+      if (u >= S2) {
+        meet();
+        ok = wait(b_free2[s], u / S2 - 1);
+      } else {
+        // the places of the first product that lie here: their last stages
+        for (int q = s * C::kStage2Bytes / C::kStageBytes;
+             q <= ((s + 1) * C::kStage2Bytes - 1) / C::kStageBytes; ++q)
+          if (q < n_a) ok = wait(b_free[q], (n_a - 1 - q) / S) && ok;
+      }
+      if (!ok) break;
+      const uint32_t st = at_stage2(u), full = smem_u32(&b_full2[s]);
+      const int n = 64 * (s0 + u);
+      if (pt == 0) {
+        mbar_arrive_expect_tx(full, C::kOpBytes);
+        tma_load_2d(st + C::kYBytes, &map_b, 0, adapter * p.N + n, full);
+        if constexpr (R == 128)
+          tma_load_2d(st + C::kYBytes + 8192, &map_b, 64, adapter * p.N + n, full);
+      }
+      if (n + ych * 8 < p.N) {
+#pragma unroll
+        for (int i = 0; i < YI; ++i) {
+          cp_async16(st + yto + i * YS * 128, rp[i]);
+          rp[i] += 128;
+        }
+      }
+      cp_async_arrive(full);
+      __syncwarp();
+    }
+    meet();
+    cp_async_commit();
+    cp_async_wait<0>();
+    if (*abort) {  // wait for what is under way
+      for (int i = max(0, t - S); i < t; ++i)
+        mbar_wait(smem_u32(&b_full[i % S]), (i / S) & 1, nullptr, kDrainLimitNs);
+      for (int i = max(0, u - S2); i < u; ++i)
+        mbar_wait(smem_u32(&b_full2[i % S2]), (i / S2) & 1, nullptr, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA
+    if (p.ctas > 1) cluster_arrive();
+    const bool leader = elect_one();
+    for (int t = 0; t < n_a; ++t) {
+      const int s = t % S;
+      if (!wait(b_xfull[t & 1], t >> 1)) break;
+      if (!wait(b_full[s], t / S)) break;
+      tc_fence_after();
+      if (leader) {
+        constexpr uint32_t id = idesc_bf16(TM, R);
+        const uint32_t st = at_stage(t);
+        const uint64_t a = smem_desc_sw128(st + C::kXBytes);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t xa = tmem + kSlots + (t & 1) * 64 + (ks / 2) * 32 + (ks % 2) * 8;
+          mma_bf16_ts(tmem + kD1, xa, a + 2 * ks, id, t > 0 || ks > 0);
+          if constexpr (!BF16X) mma_bf16_ts(tmem + kD1, xa + 16, a + 2 * ks, id, 1);
+        }
+        tc_commit(smem_u32(&b_free[s]));
+        tc_commit(smem_u32(&b_xfree[t & 1]));
+      }
+      __syncwarp();
+    }
+    if (leader) tc_commit(smem_u32(&b_d1));
+    __syncwarp();
+    if (p.ctas > 1) {
+      cluster_wait();
+      cluster_sync_all();
+    }
+    const int ksteps = (p.rank + 15) / 16;
+    if (wait(b_t, 0)) {
+      for (int u = 0; u < n_b; ++u) {
+        if (!wait(b_full2[u % S2], u / S2)) break;
+        if (u >= 2 && !wait(b_dfree[u & 1], (u >> 1) - 1)) break;
+        tc_fence_after();
+        if (leader) {
+          constexpr uint32_t id = idesc_bf16(TM, 64);
+          const uint64_t b = smem_desc_sw128(at_stage2(u) + C::kYBytes);
+          const uint32_t d = tmem + kD2 + (u & 1) * 64;
+          for (int ks = 0; ks < ksteps; ++ks) {
+            // (64 ranks a tile of 64 columns; the next 64 in the next tile)
+            const uint64_t bk = b + (ks / 4) * (64 * 128 / 16) + 2 * (ks % 4);
+            mma_bf16_ts(d, tmem + kT + ks * 8, bk, id, ks > 0);
+            mma_bf16_ts(d, tmem + kT + R / 2 + ks * 8, bk, id, 1);
+          }
+          tc_commit(smem_u32(&b_dfull[u & 1]));
+        }
+        __syncwarp();
+      }
+    }
+    if (*abort) {  // MMAs may still run: one more commit, which tracks them all
+      if (leader) tc_commit(smem_u32(&b_end));
+      mbar_wait(smem_u32(&b_end), 0, nullptr, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- workers
+    // a thread's row of the tile (its lane of tensor memory), and its quarter
+    // of whatever the row has
+    const int row = tid & (TM - 1), quarter = tid >> 7;
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);
+    for (int t = 0; t < n_a; ++t) {
+      if (!wait(b_full[t % S], t / S)) break;
+      if (t >= 2 && !wait(b_xfree[t & 1], (t >> 1) - 1)) break;
+      tc_fence_after();
+      uint32_t hi[8], lo[8];
+      if constexpr (BF16X) {
+        const uint32_t x = at_stage(t) + row * 128;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 v = lds128(x + (((quarter * 2 + c) ^ (row & 7)) << 4));
+          hi[4 * c] = v.x;
+          hi[4 * c + 1] = v.y;
+          hi[4 * c + 2] = v.z;
+          hi[4 * c + 3] = v.w;
+        }
+      } else {
+        const uint32_t x = at_stage(t) + (quarter / 2) * (TM * 128) + row * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = lds128(x + ((((quarter & 1) * 4 + c) ^ (row & 7)) << 4));
+          split_bf16(__uint_as_float(v.x), __uint_as_float(v.y), hi[2 * c], lo[2 * c]);
+          split_bf16(__uint_as_float(v.z), __uint_as_float(v.w), hi[2 * c + 1], lo[2 * c + 1]);
+        }
+      }
+      const uint32_t to = mine + kSlots + (t & 1) * 64 + (quarter / 2) * 32 + (quarter & 1) * 8;
+      tmem_st_x8(to, hi);
+      if constexpr (!BF16X) tmem_st_x8(to + 16, lo);
+      tmem_wait_st();
+      tc_fence_before();
+      arrive(b_xfull[t & 1]);
+    }
+    wait(b_d1, 0);
+    tc_fence_after();
+
+    // the cluster's sums, in a fixed order; ranks past p.rank and rows past
+    // cnt are zero
+    const float scale = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
+    float v[Q];
+#pragma unroll
+    for (int i = 0; i < Q; i += 16) {
+      uint32_t u[16];
+      tmem_ld_x16(mine + kD1 + quarter * Q + i, u);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[i + j] = __uint_as_float(u[j]);
+    }
+    if (p.ctas > 1) {
+      const uint32_t at = sums + (row * RP + quarter * Q) * 4;
+#pragma unroll
+      for (int i = 0; i < Q; i += 4)
+        sts128(at + i * 4, make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                      __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])));
+      cluster_sync_all();
+      // Whole rows at a time: a warp that reads 32 rows' quarters from a peer
+      // takes 10 us and more for what takes one this way.
+      constexpr int E = TM * (R / 4) / NW;
+      float4 w[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = tid + e * NW, r = i / (R / 4), ch = i % (R / 4);
+        w[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < cnt && ch * 4 < p.rank) {
+          for (int q = 0; q < p.ctas; ++q) {
+            const int4 u = dsmem_ld_v4(dsmem_map(sums + (r * RP + ch * 4) * 4, q));
+            w[e].x += __int_as_float(u.x);
+            w[e].y += __int_as_float(u.y);
+            w[e].z += __int_as_float(u.z);
+            w[e].w += __int_as_float(u.w);
+          }
+        }
+      }
+      __syncwarp();
+      cluster_sync_all();  // every CTA has read: the totals take the parts' place
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = tid + e * NW, r = i / (R / 4), ch = i % (R / 4);
+        sts128(sums + (r * RP + ch * 4) * 4,
+               make_uint4(__float_as_uint(w[e].x), __float_as_uint(w[e].y),
+                          __float_as_uint(w[e].z), __float_as_uint(w[e].w)));
+      }
+      named_bar_sync(1, NW);
+#pragma unroll
+      for (int i = 0; i < Q; i += 4) {
+        const uint4 u = lds128(at + i * 4);
+        v[i] = __uint_as_float(u.x);
+        v[i + 1] = __uint_as_float(u.y);
+        v[i + 2] = __uint_as_float(u.z);
+        v[i + 3] = __uint_as_float(u.w);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < Q; i += 16) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = quarter * Q + i + 2 * j;
+        const bool in = row < cnt && k < p.rank;  // (p.rank is even)
+        split_bf16(in ? v[i + 2 * j] * scale : 0.0f, in ? v[i + 2 * j + 1] * scale : 0.0f, hi[j],
+                   lo[j]);
+      }
+      tmem_st_x8(mine + kT + (quarter * Q + i) / 2, hi);
+      tmem_st_x8(mine + kT + R / 2 + (quarter * Q + i) / 2, lo);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    arrive(b_t);
+
+    // Y += d, one half of the workers on even stages, the other on odd ones:
+    // half a row a thread.  (After an abort the loop runs on, as its warps
+    // meet at a barrier.)
+    const int side = warp / (NW / 64), gt = tid & (NW / 2 - 1), part = gt >> 7;
+    const int r8 = gt / 8, c8 = gt % 8;
+    for (int u = side; u < n_b; u += 2) {
+      const int n = 64 * (s0 + u);
+      const uint32_t st = at_stage2(u);
+      bool ok = wait(b_dfull[side], u >> 1);
+      ok = wait(b_full2[u % S2], u / S2) && ok;
+      tc_fence_after();
+      const uint32_t y = st + row * 128;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t d[16];
+        tmem_ld_x16(mine + kD2 + side * 64 + part * 32 + h * 16, d);
+        uint4 w[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          w[c] = lds128(y + (((part * 4 + h * 2 + c) ^ (row & 7)) << 4));
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = pack_bf16(__uint_as_float(ws[j] << 16) + __uint_as_float(d[c * 8 + 2 * j]),
+                             __uint_as_float(ws[j] & 0xffff0000u) +
+                                 __uint_as_float(d[c * 8 + 2 * j + 1]));
+          sts128(y + (((part * 4 + h * 2 + c) ^ (row & 7)) << 4),
+                 make_uint4(o[0], o[1], o[2], o[3]));
+        }
+      }
+      tc_fence_before();
+      arrive(b_dfree[side]);
+      named_bar_sync(2 + side, NW / 2);
+      if (ok && n + c8 * 8 < p.N && !*abort) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = r8 + 32 * i, m = toks[rr];
+          if (m >= 0)
+            *reinterpret_cast<uint4*>(p.Y + (size_t)m * p.ldy + n + c8 * 8) =
+                lds128(st + rr * 128 + ((c8 ^ (rr & 7)) << 4));
+        }
+      }
+      arrive(b_free2[u % S2]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+}  // namespace w4a8

@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -18,6 +19,7 @@
 #include "gemv.cuh"
 #include "layout.cuh"
 #include "lora.cuh"
+#include "lora_tc.cuh"
 #include "moe.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -1016,7 +1018,8 @@ cudaError_t launch_lora_as(const LoraParams& p, int slots, int parts, cudaStream
   constexpr int smem = LoraCfg<BF16X, NT, WR>::kSmemBytes;
   const cudaError_t e = ensure_smem(lora_kernel<BF16X, NT, WR>, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_k(lora_kernel<BF16X, NT, WR>, dim3(slots * p.ctas, parts), dim3(kLoraThreads), smem,
+  return launch_k(lora_kernel<BF16X, NT, WR>, dim3(slots * p.ctas, parts),
+                  dim3(LoraCfg<BF16X, NT, WR>::kThreads), smem,
                   st, pdl, p.ctas, p);
 }
 
@@ -1028,11 +1031,104 @@ cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream
   return launch_lora_as<BF16X, 16, WR>(p, slots, parts, st, pdl);
 }
 
-// Row tiles of 64 where adapters have 32 rows or more on average and there
-// are tiles enough to fill the machine (8192 rows, 8192 x 8192, rank 32: 111 us
-// against 144 with tiles of 16; 1024 rows, 4096 x 4096, bf16: 21 against 16),
-// else of 16.  A tile's cluster grows while the CTAs still fit the machine
-// at once, two an SM (one more doubling is a second wave: 32 rows of 32
+// Tensor map of a row-major bf16 matrix: boxes of 64 columns by `rows` rows,
+// 128-byte swizzle, zero fill outside.
+bool make_bf16_map(CUtensorMap* map, const uint16_t* base, int cols, long long rows,
+                   int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters of `ctas` CTAs of a kernel that the machine holds at once (GPCs
+// do not divide evenly), asked once per device.
+template <typename F>
+int clusters_at_once(F* kernel, int ctas, int threads, size_t smem, int sms,
+                     std::atomic<int> (*cache)[9]) {
+  const int dev = current_device();
+  if (dev < 0 || dev >= kMaxDevices) return sms / ctas;
+  int n = cache[dev][ctas].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = sms / ctas > 0 ? sms / ctas : 1;
+  }
+  cache[dev][ctas].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// The tcgen05 form: tiles of 128 rows, one CTA an SM.  The cluster is the size
+// that wastes least of the last wave, a CTA costing about an eighth of a tile
+// beside its share of it (8192 x 8192, rank 64, fp32 x: 6000 rows 99 us with 2
+// CTAs a tile and 133 with 3, a second wave; 4096 rows 92 with 2 and 73 with
+// 3).  How many tiles there are is known on the device only: half a tile per
+// adapter is likely left over.
+template <bool BF16X, int R>
+cudaError_t launch_lora_tc_as(LoraParams p, int used, int sms, cudaStream_t st, bool pdl) {
+  static std::atomic<bool> done[kMaxDevices];
+  static std::atomic<int> room[kMaxDevices][9];
+  constexpr int smem = LoraTcCfg<BF16X, R>::kSmemBytes, tm = kLoraTcRows;
+  const cudaError_t e = ensure_smem(lora_tc_kernel<BF16X, R>, smem, done);
+  if (e != cudaSuccess) return e;
+  CUtensorMap a, b;
+  if (!make_bf16_map(&a, p.A, p.K, (long long)p.adapters * p.rank, R) ||
+      !make_bf16_map(&b, p.B, p.rank, (long long)p.adapters * p.N, 64))
+    return cudaErrorInvalidValue;
+  const int slots = (int)(((long long)p.M + (long long)used * (tm - 1)) / tm);
+  const int tiles = (int)((double)p.M / tm + 0.5 * used + 0.7 * std::sqrt((double)used));
+  double best = 1e30;
+  for (int c = 1; c <= 8 && c <= p.K / 64; ++c) {
+    const int at_once =
+        clusters_at_once(lora_tc_kernel<BF16X, R>, c, kLoraTcThreads, smem, sms, room);
+    const double t = (double)((tiles + at_once - 1) / at_once) * (1.0 / c + 1.0 / 8);
+    if (t < best - 1e-9) {
+      best = t;
+      p.ctas = c;
+    }
+  }
+  return launch_k(lora_tc_kernel<BF16X, R>, dim3(slots * p.ctas), dim3(kLoraTcThreads), smem, st,
+                  pdl, p.ctas, a, b, p, wait_budget());
+}
+
+cudaError_t launch_lora_tc(const LoraParams& p, bool bf16x, int sms, int used, cudaStream_t st,
+                           bool pdl) {
+  if (p.rank <= 64)
+    return bf16x ? launch_lora_tc_as<true, 64>(p, used, sms, st, pdl)
+                 : launch_lora_tc_as<false, 64>(p, used, sms, st, pdl);
+  return bf16x ? launch_lora_tc_as<true, 128>(p, used, sms, st, pdl)
+               : launch_lora_tc_as<false, 128>(p, used, sms, st, pdl);
+}
+
+// Many rows and ranks over 32 take the tcgen05 form (lora_tc.cuh); it starts
+// slower, so it waits for 131072 rows x ranks (8192 x 10240, fp32 x, tcgen05
+// against the warp MMAs: rank 64, 1024 rows 42 us against 36, 2048 rows 51
+// against 60, 3000 rows of 30 adapters 79 against 107; rank 128, 512 rows 52
+// against 36, 1024 rows 56 against 61), and for ranks up to 32, bound by
+// their bytes either way, it never gains (8192 rows, 8192 x 8192, rank 32: 115
+// against 112).
+//
+// Otherwise row tiles of 64 where adapters have 32 rows or more on average and
+// there are tiles enough to fill the machine (8192 rows, 8192 x 8192, rank 32:
+// 112 us against 144 with tiles of 16; 1024 rows, 4096 x 4096, bf16: 21
+// against 16), else of 16.  A tile's cluster grows while the CTAs still fit
+// the machine at once (one more doubling is a second wave: 32 rows of 32
 // adapters, 8192 x 10240, rank 64, take 20 us with 256 CTAs, 30 with 512, 35
 // with 64), a CTA keeping 256 k.  With few tiles N is split further, which
 // repeats the first product: one row, 4096 x 12288: 8.1 us with 64 CTAs, 9.4
@@ -1040,11 +1136,15 @@ cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream
 // 10.8 with 256).
 cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool pdl) {
   const int used = p.adapters < p.M ? p.adapters : p.M;
+  if (p.rank > 32 && p.M / used >= 64 && (long long)p.rank * p.M >= 131072 && !p.ids &&
+      p.y_vec && p.N % 8 == 0 && (long long)p.adapters * p.N < (1ll << 31))
+    return launch_lora_tc(p, bf16x, sms, used, st, pdl);
   const bool tall = p.M / used >= 32 && p.M / 64 >= sms / 3;
   const int tm = tall ? 64 : 16;
   const int slots = (int)(((long long)p.M + (long long)used * (tm - 1)) / tm);
   int ctas = 1, parts = 1;
-  while (ctas < 8 && (long long)slots * ctas * 2 <= 2 * sms && p.K >= 512 * ctas) ctas *= 2;
+  const int fit = p.rank > 64 ? sms : 2 * sms;  // CTAs at once
+  while (ctas < 8 && (long long)slots * ctas * 2 <= fit && p.K >= 512 * ctas) ctas *= 2;
   while (slots * ctas * parts * 4 <= sms && p.N >= 256 * ctas * parts) parts *= 2;
   p.ctas = ctas;
   if (tall)

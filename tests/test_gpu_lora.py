@@ -59,7 +59,10 @@ def check(Y0, Y1, X, A, B, ids, scale):
     (700, 384, 96, 24, 300, False), (300, 256, 64, 8, 1024, False), (5000, 256, 40, 32, 12, True),
     # planned, in tall tiles
     (3300, 256, 72, 16, 5, True), (3300, 128, 264, 64, 4, True), (3250, 384, 33, 128, 3, True),
-    (3300, 128, 96, 104, 2, False), (3200, 640, 130, 8, 100, True), (3200, 4096, 320, 48, 1, True)])
+    (3300, 128, 96, 104, 2, False), (3200, 640, 130, 8, 100, True), (3200, 4096, 320, 48, 1, True),
+    # planned, on the tcgen05 tensor cores
+    (1100, 1024, 200, 128, 3, True), (2100, 4096, 1000, 64, 5, False), (1300, 128, 8, 120, 1, False),
+    (4000, 640, 2056, 40, 30, True), (2048, 192 * 2, 64, 72, 16, True), (9001, 256, 96, 56, 2, True)])
 def test_lora(M, K, N, r, L, runs, dtype):
     A, B, scale = _weights(L, K, N, r, 10 * M + r)
     X = wl.random_matrix(M, K, M + K, kind="heavy").to(dtype).cuda()
@@ -106,6 +109,46 @@ def test_lora_strides_and_neighbours():
             assert torch.equal(big.view(torch.int16), before.view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_lora_strides_of_many_rows(dtype):
+    M, K, N, r, L = 2300, 512, 192, 64, 4
+    ids = _ids(M, L, 14, True)
+    d = torch.from_numpy(ids).cuda()
+    A, B, scale = _weights(L, K, N, r, 15)
+    X = wl.random_matrix(M, K + 64, 16).to(dtype).cuda()[:, 32:32 + K]
+    big = wl.random_matrix(M, N + 72, 17).bfloat16().cuda()
+    before = big.clone()
+    for y0 in (0, 8, 72, 3):     # (3: not aligned, so not the tensor-core form)
+        w4.w4a8_lora(X, big[:, y0:y0 + N], A, B, d, scale=scale)
+        check(before[:, y0:y0 + N], big[:, y0:y0 + N], X, A, B, ids, scale)
+        big[:, y0:y0 + N] = before[:, y0:y0 + N]
+        assert torch.equal(big.view(torch.int16), before.view(torch.int16))
+
+
+def test_lora_tensor_core_form_gives_up_cleanly():
+    """With a wait budget of 0 the call stores nothing and the status says so;
+    the next call works."""
+    M, K, N, r, L = 2300, 512, 192, 64, 4
+    ids = torch.from_numpy(_ids(M, L, 18, True)).cuda()
+    A, B, scale = _weights(L, K, N, r, 19)
+    X = wl.random_matrix(M, K, 20).cuda()
+    Y0 = wl.random_matrix(M, N, 21).bfloat16().cuda()
+    want = w4.w4a8_lora(X, Y0.clone(), A, B, ids, scale=scale)
+    Y = Y0.clone()
+    torch.cuda.synchronize()
+    w4.w4a8_debug_set_wait_budget(0)
+    try:
+        w4.w4a8_lora(X, Y, A, B, ids, scale=scale)
+        torch.cuda.synchronize()
+    finally:
+        w4.w4a8_debug_set_wait_budget(-1)
+    assert w4.w4a8_get_status() == w4.ERR_TIMEOUT
+    assert torch.equal(Y.view(torch.int16), Y0.view(torch.int16))
+    w4.w4a8_lora(X, Y, A, B, ids, scale=scale)
+    assert torch.equal(Y.view(torch.int16), want.view(torch.int16))
+    assert w4.w4a8_get_status() == 0
+
+
 def test_lora_no_rows_and_no_adapter():
     A, B, scale = _weights(3, 128, 64, 8, 1)
     X = wl.random_matrix(6, 128, 2).cuda()
@@ -138,10 +181,11 @@ def test_lora_precision_is_above_one_bf16_term():
     assert np.all(err <= 2.0 ** -8 * np.abs(t) + (2.0 ** -16 + (K / 8 + 32) * 2.0 ** -22) * mag)
 
 
-def test_lora_is_deterministic_and_a_plan_is_shared():
+@pytest.mark.parametrize("M,r", [(600, 32), (2500, 64)])
+def test_lora_is_deterministic_and_a_plan_is_shared(M, r):
     """Two layers with one plan on two streams at once, and twice: the same
     bits as one after the other."""
-    M, K, N, r, L = 600, 512, 512, 32, 7
+    K, N, L = 512, 512, 7
     ids = torch.from_numpy(_ids(M, L, 8, True)).cuda()
     plan = w4.w4a8_lora_plan(ids, L)
     layers = [_weights(L, K, N, r, 30 + i) for i in range(2)]
@@ -158,12 +202,12 @@ def test_lora_is_deterministic_and_a_plan_is_shared():
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
-@pytest.mark.parametrize("M", [3, 200, 900])
+@pytest.mark.parametrize("M,r", [(3, 16), (200, 16), (900, 16), (2200, 64)])
 @pytest.mark.parametrize("flags", [0, w4.W4A8_FLAG_PDL])
-def test_lora_beside_the_projection_captured_and_replayed(M, flags):
+def test_lora_beside_the_projection_captured_and_replayed(M, r, flags):
     """Quantize, W4A8 GEMM, adapters: captured, replayed for other requests'
     ids and inputs, against the GEMM's own output plus the adapters."""
-    K, N, r, L = 512, 384, 16, 6
+    K, N, L = 512, 384, 6
     W = wl.random_matrix(N, K, 40, std=0.02).cuda()
     pk = w4.w4a8_quantize_weights(W)
     A, B, scale = _weights(L, K, N, r, 41)
