@@ -188,44 +188,66 @@ lora_kernel(const LoraParams p) {
   __shared__ int toks[TM];
   int adapter = -1, cnt = 0;
   if (WR == 1 && p.ids != nullptr) {
-    // few rows (one per thread), not grouped yet: a row that has a multiple
+    // Few rows (one per thread), not grouped yet: a row that has a multiple
     // of TM rows of its adapter before it opens a tile, and tiles count in
-    // the order of the rows that open them
-    __shared__ __align__(16) int sid[kLoraIdsMax];
-    __shared__ int opens[NTHR / 32];
-    __shared__ int found[3];  // adapter, first rank, rows
+    // the order of the rows that open them.
     int id = tid < p.M ? p.ids[tid] : -1;
+    if (p.M <= 32) id = lane < p.M ? p.ids[lane] : -1;  // every warp the same rows
     if ((unsigned)id >= (unsigned)p.adapters) id = -1;
-    sid[tid] = id;
-    if (tid < TM) toks[tid] = -1;
-    if (tid < 3) found[tid] = tid == 0 ? -1 : 0;
-    __syncthreads();
-    int before = 0;
-    for (int i = 0; i < tid; i += 4) {
-      const int4 v = *reinterpret_cast<const int4*>(sid + i);
-      before += (v.x == id) + (v.y == id && i + 1 < tid) + (v.z == id && i + 2 < tid) +
-                (v.w == id && i + 3 < tid);
+    const unsigned lower = (1u << lane) - 1;
+    int before = __popc(__match_any_sync(0xffffffffu, id) & lower);
+    if (p.M <= 32) {
+      const bool open = id >= 0 && before % TM == 0;
+      const unsigned mask = __ballot_sync(0xffffffffu, open);
+      const unsigned hit =
+          __ballot_sync(0xffffffffu, open && __popc(mask & lower) == slot);
+      if (hit == 0) return;  // the whole cluster: a slot past the last tile
+      const int src = __ffs(hit) - 1;
+      adapter = __shfl_sync(0xffffffffu, id, src);
+      const int r = before - __shfl_sync(0xffffffffu, before, src);
+      const bool in = id == adapter && (unsigned)r < (unsigned)TM;
+      cnt = __popc(__ballot_sync(0xffffffffu, in));
+      if (warp == 0) {
+        if (lane < TM) toks[lane] = -1;
+        __syncwarp();
+        if (in) toks[r] = lane;
+      }
+      __syncthreads();
+    } else {
+      __shared__ __align__(16) int sid[kLoraIdsMax];
+      __shared__ int opens[NTHR / 32];
+      __shared__ int found[3];  // adapter, first rank, rows
+      sid[tid] = id;
+      if (tid < TM) toks[tid] = -1;
+      if (tid < 3) found[tid] = tid == 0 ? -1 : 0;
+      __syncthreads();
+      if (warp * 32 < p.M) {  // the warps before
+        for (int i = 0; i < warp * 32; i += 4) {
+          const int4 v = *reinterpret_cast<const int4*>(sid + i);
+          before += (v.x == id) + (v.y == id) + (v.z == id) + (v.w == id);
+        }
+      }
+      const bool open = id >= 0 && before % TM == 0;
+      const unsigned mask = __ballot_sync(0xffffffffu, open);
+      if (lane == 0) opens[warp] = __popc(mask);
+      __syncthreads();
+      int at = __popc(mask & lower);
+      for (int w = 0; w < warp; ++w) at += opens[w];
+      if (open && at == slot) {
+        found[0] = id;
+        found[1] = before;
+      }
+      __syncthreads();
+      adapter = found[0];
+      if (adapter < 0) return;  // the whole cluster: a slot past the last tile
+      const int r = before - found[1];
+      if (id == adapter && (unsigned)r < (unsigned)TM) {
+        toks[r] = tid;
+        atomicAdd(found + 2, 1);
+      }
+      __syncthreads();
+      cnt = found[2];
     }
-    const bool open = id >= 0 && before % TM == 0;
-    const unsigned mask = __ballot_sync(0xffffffffu, open);
-    if (lane == 0) opens[warp] = __popc(mask);
-    __syncthreads();
-    int at = __popc(mask & ((1u << lane) - 1));
-    for (int w = 0; w < warp; ++w) at += opens[w];
-    if (open && at == slot) {
-      found[0] = id;
-      found[1] = before;
-    }
-    __syncthreads();
-    adapter = found[0];
-    if (adapter < 0) return;  // the whole cluster: a slot past the last tile
-    const int r = before - found[1];
-    if (id == adapter && (unsigned)r < (unsigned)TM) {
-      toks[r] = tid;
-      atomicAdd(found + 2, 1);
-    }
-    __syncthreads();
-    cnt = found[2];
   } else {
     adapter = lora_tile<TM>(p, slot, tid, toks, cnt);
     if (adapter < 0) return;  // the whole cluster: a slot past the last tile

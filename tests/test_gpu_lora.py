@@ -51,7 +51,8 @@ def check(Y0, Y1, X, A, B, ids, scale):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,K,N,r,L,runs", [
     (1, 128, 1, 8, 1, False), (1, 4096, 4096, 16, 4, False), (2, 256, 33, 24, 3, False),
-    (5, 384, 200, 40, 7, False), (16, 1024, 96, 64, 2, False), (17, 512, 70, 128, 1, False),
+    (5, 384, 200, 40, 7, False), (16, 1024, 96, 64, 2, False), (17, 512, 70, 128, 1, False), (32, 256, 64, 16, 1, False),
+    (31, 384, 40, 24, 2, True), (33, 256, 64, 16, 1, False), (32, 256, 96, 8, 40, False),
     (64, 2048, 512, 16, 64, False), (255, 640, 264, 32, 5, False), (256, 256, 128, 104, 9, True),
     (256, 256, 72, 8, 1, False),
     # planned
