@@ -302,8 +302,9 @@ int w4a8_gemm_variant(int variant, const int8_t* Xq, const float* s_x,
  *            w4a8_packed_weight_bytes(N, K, group) bytes apart (group g's
  *            buffer starts g times that many bytes after `packed`).
  *   offsets: int32 [groups + 1] on the DEVICE: offsets[0] = 0, nondecreasing,
- *            offsets[groups] = M_total.  It may be written by the preceding
- *            kernel in the stream (with W4A8_FLAG_PDL the kernel waits for it).
+ *            offsets[groups] <= M_total; rows from there on belong to no
+ *            group and their Y is left as it was.  It may be written by the
+ *            preceding kernel in the stream (with W4A8_FLAG_PDL the kernel waits for it).
  *   max_rows: host-side bound on the rows of any one group (1..M_total);
  *            it sizes the launch and the tile width, so a tight bound is
  *            faster.  Xq [M_total][K], s_x [M_total], Y [M_total][N].
@@ -418,6 +419,8 @@ int w4a8_moe_combine(const uint16_t* Y, int rows, int N, const int32_t* pos,
  *   or NULL (all 1).
  * Sums are fp32.  fp32 X and A x enter the products as two bf16 terms
  * each (16 bits of them); the sum with Y is rounded once.  |X| < 3.38e38.
+ * Many rows with ranks over 32 run on the tcgen05 tensor cores; a wait of
+ * theirs that runs out is reported by w4a8_get_status, as the GEMMs' are.
  * The rows are given in one of two ways:
  *   ids [M] int32, offsets = rows = NULL: for M <= 256;
  *   ids = NULL, offsets and rows from w4a8_lora_plan for these ids.
