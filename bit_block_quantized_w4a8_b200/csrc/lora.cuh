@@ -6,9 +6,10 @@
 // One launch does both products.  Rows are taken in tiles that share an
 // adapter: the grouped order of group_rows_kernel, or for a few rows the
 // order that each CTA finds from the ids by itself (a launch less).  A
-// cluster of CTAs owns a tile: each CTA multiplies its stretch of K (t = A x, summed over the
-// CTA's warps in shared memory and over the cluster through distributed
-// shared memory), then updates its stretch of N.  t never leaves the chip.
+// cluster of CTAs owns a tile: each CTA multiplies its stretch of K (t = A x,
+// summed over the CTA's warps in shared memory and over the cluster through
+// distributed shared memory), then updates its stretch of N.  t never leaves
+// the chip.
 //
 // Bound by HBM (X once, Y twice, A and B once per adapter and tile, mostly
 // from L2): at ranks up to 32 the tensor work is well below the bytes, and

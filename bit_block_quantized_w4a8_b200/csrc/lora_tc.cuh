@@ -70,7 +70,7 @@ struct LoraTcCfg {
   static constexpr int kStage2Bytes = kYBytes + kOpBytes;
   static constexpr int kPitch = R + 4;                                // floats per row of t
   static constexpr int kSumBytes = kLoraTcRows * kPitch * 4;
-  static constexpr int kFit = (226 * 1024 - 3072 - kSumBytes) / kStageBytes;
+  static constexpr int kFit = (223 * 1024 - kSumBytes) / kStageBytes;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kStages2 = kStages * kStageBytes / kStage2Bytes;
   static constexpr int kSmemBytes = kStages * kStageBytes + kSumBytes + 1024;  // (1024: alignment)
