@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -1074,12 +1075,17 @@ int clusters_at_once(F* kernel, int ctas, int threads, size_t smem, int sms,
   return n;
 }
 
+// Tiles of tm rows that M rows of `used` adapters likely make: half a tile per
+// adapter is left over, give or take.
+double likely_tiles(int M, int used, int tm) {
+  return (double)M / tm + 0.5 * used + 0.3 * std::sqrt((double)used);
+}
+
 // The tcgen05 form: tiles of 128 rows, one CTA an SM.  The cluster is the size
 // that wastes least of the last wave, a CTA costing about an eighth of a tile
 // beside its share of it (8192 x 8192, rank 64, fp32 x: 6000 rows 99 us with 2
 // CTAs a tile and 133 with 3, a second wave; 4096 rows 92 with 2 and 73 with
-// 3).  How many tiles there are is known on the device only: half a tile per
-// adapter is likely left over.
+// 3).  How many tiles there are is known on the device only.
 template <bool BF16X, int R>
 cudaError_t launch_lora_tc_as(LoraParams p, int used, int sms, cudaStream_t st, bool pdl) {
   static std::atomic<bool> done[kMaxDevices];
@@ -1092,7 +1098,7 @@ cudaError_t launch_lora_tc_as(LoraParams p, int used, int sms, cudaStream_t st, 
       !make_bf16_map(&b, p.B, p.rank, (long long)p.adapters * p.N, 64))
     return cudaErrorInvalidValue;
   const int slots = (int)(((long long)p.M + (long long)used * (tm - 1)) / tm);
-  const int tiles = (int)((double)p.M / tm + 0.5 * used + 0.7 * std::sqrt((double)used));
+  const int tiles = (int)likely_tiles(p.M, used, tm);
   double best = 1e30;
   for (int c = 1; c <= 8 && c <= p.K / 64; ++c) {
     const int at_once =
@@ -1116,6 +1122,28 @@ cudaError_t launch_lora_tc(const LoraParams& p, bool bf16x, int sms, int used, c
                : launch_lora_tc_as<false, 128>(p, used, sms, st, pdl);
 }
 
+// Cluster of a tall tile: whole waves of CTAs run at what HBM gives (5.3 TB/s
+// of reads and writes), the last at that or at 29 GB/s a CTA, and a wave costs
+// 4 us beside.  5000 rows, 8192 x 8192, fp32 x, rank 16: 71 us with 3, 83 with
+// 2, 90 with 4; 9000 rows, rank 32: 119 with 2, 141 with 3; 10000 rows, 4096 x
+// 4096, bf16 x: 63 with 3, 66 with 1 or 2.
+int tall_cluster(const LoraParams& p, bool bf16x, double tiles, int at_once) {
+  const double bytes = (double)p.M * ((bf16x ? 2.0 : 4.0) * p.K + 4.0 * p.N);
+  double best = 1e30;
+  int ctas = 1;
+  for (int c = 1; c <= 8 && c <= p.K / 128; ++c) {
+    const int n = (int)(tiles * c), full = n / at_once, rest = n - full * at_once;
+    const double each = bytes / n;
+    const double t = full * (at_once * each / 5.3e6 + 4.0) +
+                     (rest ? std::max(rest * each / 5.3e6, each / 29e3) + 4.0 : 0.0);
+    if (t < best) {
+      best = t;
+      ctas = c;
+    }
+  }
+  return ctas;
+}
+
 // Many rows and ranks over 32 take the tcgen05 form (lora_tc.cuh); it starts
 // slower, so it waits for 131072 rows x ranks (8192 x 10240, fp32 x, tcgen05
 // against the warp MMAs: rank 64, 1024 rows 42 us against 36, 2048 rows 51
@@ -1127,8 +1155,8 @@ cudaError_t launch_lora_tc(const LoraParams& p, bool bf16x, int sms, int used, c
 // Otherwise row tiles of 64 where adapters have 32 rows or more on average and
 // there are tiles enough to fill the machine (8192 rows, 8192 x 8192, rank 32:
 // 112 us against 144 with tiles of 16; 1024 rows, 4096 x 4096, bf16: 21
-// against 16), else of 16.  A tile's cluster grows while the CTAs still fit
-// the machine at once (one more doubling is a second wave: 32 rows of 32
+// against 16), else of 16, whose cluster grows while the CTAs still fit the
+// machine at once (one more doubling is a second wave: 32 rows of 32
 // adapters, 8192 x 10240, rank 64, take 20 us with 256 CTAs, 30 with 512, 35
 // with 64), a CTA keeping 256 k.  With few tiles N is split further, which
 // repeats the first product: one row, 4096 x 12288: 8.1 us with 64 CTAs, 9.4
@@ -1145,6 +1173,7 @@ cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool
   int ctas = 1, parts = 1;
   const int fit = p.rank > 64 ? sms : 2 * sms;  // CTAs at once
   while (ctas < 8 && (long long)slots * ctas * 2 <= fit && p.K >= 512 * ctas) ctas *= 2;
+  if (tall) ctas = tall_cluster(p, bf16x, likely_tiles(p.M, used, tm), fit);
   while (slots * ctas * parts * 4 <= sms && p.N >= 256 * ctas * parts) parts *= 2;
   p.ctas = ctas;
   if (tall)

@@ -59,7 +59,8 @@ def check(Y0, Y1, X, A, B, ids, scale):
     (257, 256, 136, 16, 4, False), (400, 1152, 301, 64, 3, True), (1000, 128, 64, 128, 2, True),
     (700, 384, 96, 24, 300, False), (300, 256, 64, 8, 1024, False), (5000, 256, 40, 32, 12, True),
     # planned, in tall tiles
-    (3300, 256, 72, 16, 5, True), (3300, 128, 264, 64, 4, True), (3250, 384, 33, 128, 3, True),
+    (3300, 256, 72, 16, 5, True), (5000, 1152, 64, 16, 3, True), (10000, 640, 40, 32, 2, False),
+    (3300, 1024, 64, 8, 1, True), (3300, 128, 264, 64, 4, True), (3250, 384, 33, 128, 3, True),
     (3300, 128, 96, 104, 2, False), (3200, 640, 130, 8, 100, True), (3200, 4096, 320, 48, 1, True),
     # planned, on the tcgen05 tensor cores
     (1100, 1024, 200, 128, 3, True), (2100, 4096, 1000, 64, 5, False), (1300, 128, 8, 120, 1, False),
