@@ -240,6 +240,23 @@ def test_lora_beside_the_projection_captured_and_replayed(M, r, flags):
     del graph
 
 
+@pytest.mark.parametrize("r", [16, 64])
+def test_lora_offsets_past_32_bits(r):
+    """X and Y of more than 2^31 elements, in the warp-level and in the
+    tensor-core form."""
+    M, K, N, L = 270001, 8192, 8192, 2
+    A, B, scale = _weights(L, K, 64, r, 60)
+    B = B.repeat(1, N // 64, 1).contiguous()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    X = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    Y = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    assert X.numel() > 2 ** 31 and Y.numel() > 2 ** 31
+    ids = torch.arange(M, device="cuda", dtype=torch.int32) // 4999 % 3 - 1
+    w4.w4a8_lora(X, Y, A, B, ids, scale=scale)
+    at = torch.tensor([0, 4999, 5000, 9998, M // 2, M - 5000, M - 2, M - 1], device="cuda")
+    check(torch.zeros_like(Y[at]), Y[at], X[at], A, B, ids[at].cpu().numpy(), scale)
+
+
 def test_lora_refusals():
     A, B, scale = _weights(2, 128, 16, 8, 50)
     X = torch.zeros(4, 128, device="cuda")

@@ -368,3 +368,29 @@ def test_moe_layer_in_a_graph_and_on_another_stream():
     for a, ref in zip(got, want):
         assert torch.equal(a, ref)
     torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """Rows, codes and outputs that lie more than 2^31 elements in."""
+    M, K, k, E = 70001, 4096, 8, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    logits = torch.randn(M, E, generator=g, device="cuda")
+    ids, w = w4.w4a8_moe_route(logits, k)
+    d = w4.w4a8_moe_dispatch(X, ids, E)
+    assert d.Xq.numel() > 2 ** 31 and int(d.offsets[-1]) == M * k
+    at = torch.tensor([0, 1, 12345, M * k // 2, M * k - 2, M * k - 1], device="cuda")
+    pairs = d.rows[at].long()
+    assert torch.equal(d.pos.view(-1)[pairs].long(), at)
+    Xq, sx = oracle.quantize_act(X[pairs // k].float().cpu().numpy())
+    assert np.array_equal(d.Xq[at].cpu().numpy(), Xq)
+    assert np.array_equal(d.s_x[at].cpu().numpy(), sx)
+    del X
+    Y = torch.randn(M * k, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    out = w4.w4a8_moe_combine(Y, d.pos, w, dtype=torch.float32)
+    some = torch.tensor([0, 7, M // 2, M - 1], device="cuda")
+    pos, ws = d.pos[some].cpu().numpy(), w[some].cpu().numpy()
+    rows = d.pos[some].long().view(-1)
+    ref, mag = plain.combine(Y[rows].float().cpu().numpy(),
+                             np.arange(pos.size).reshape(pos.shape), ws)
+    assert np.all(np.abs(out[some].double().cpu().numpy() - ref) <= k * 2.0 ** -23 * mag)
