@@ -572,12 +572,25 @@ def w4a8_moe_dispatch(X, ids, experts, out=None, stream=None, flags=0):
                           _new(stream, (M * k,), _torch.int32, d),
                           _new(stream, (M, k), _torch.int32, d))
     else:
-        d = X.get_device()
-        _need_out(out.Xq, _torch.int8, (M * k, K), d, "out.Xq")
-        _need_out(out.s_x, _torch.float32, (M * k,), d, "out.s_x")
-        _need_out(out.offsets, _torch.int32, (E + 1,), d, "out.offsets")
-        _need_out(out.rows, _torch.int32, (M * k,), d, "out.rows")
-        _need_out(out.pos, _torch.int32, (M, k), d, "out.pos")
+        d, n = X.get_device(), M * k
+        Xq, s_x, off, rows, pos = out.Xq, out.s_x, out.offsets, out.rows, out.pos
+        try:  # (one expression: five calls of the helper take a microsecond more)
+            ok = (Xq.dtype == _torch.int8 and s_x.dtype == _torch.float32
+                  and off.dtype == rows.dtype == pos.dtype == _torch.int32
+                  and Xq.shape == (n, K) and s_x.shape == (n,) and off.shape == (E + 1,)
+                  and rows.shape == (n,) and pos.shape == (M, k)
+                  and Xq.get_device() == s_x.get_device() == off.get_device()
+                  == rows.get_device() == pos.get_device() == d
+                  and Xq.is_contiguous() and s_x.is_contiguous() and off.is_contiguous()
+                  and rows.is_contiguous() and pos.is_contiguous())
+        except AttributeError:
+            ok = False
+        if not ok:
+            _need_out(Xq, _torch.int8, (n, K), d, "out.Xq")
+            _need_out(s_x, _torch.float32, (n,), d, "out.s_x")
+            _need_out(off, _torch.int32, (E + 1,), d, "out.offsets")
+            _need_out(rows, _torch.int32, (n,), d, "out.rows")
+            _need_out(pos, _torch.int32, (M, k), d, "out.pos")
     rc = lib().w4a8_moe_dispatch(X.data_ptr(), kind, M, K, ids.data_ptr(), k, E,
                                  out.Xq.data_ptr(), out.s_x.data_ptr(), out.offsets.data_ptr(),
                                  out.rows.data_ptr(), out.pos.data_ptr(), flags, st)

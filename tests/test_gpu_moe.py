@@ -230,6 +230,12 @@ def test_dispatch_of_no_tokens_and_refusals():
         w4.w4a8_moe_dispatch(X, ids, 1025)
     with pytest.raises(TypeError):
         w4.w4a8_moe_dispatch(X, ids, 4, out=w4.w4a8_moe_dispatch(X, ids, 5))
+    d = w4.w4a8_moe_dispatch(X, ids, 4)
+    for bad in (dict(Xq=None), dict(s_x=d.s_x.double()), dict(pos=d.pos.cpu()), dict(rows=d.rows[:7]),
+                dict(pos=d.pos.t()), dict(offsets=[0] * 5)):
+        parts = dict(Xq=d.Xq, s_x=d.s_x, offsets=d.offsets, rows=d.rows, pos=d.pos)
+        with pytest.raises(TypeError):
+            w4.w4a8_moe_dispatch(X, ids, 4, out=w4.MoEDispatch(**dict(parts, **bad)))
 
 
 # ---------------------------------------------------------------- combine
