@@ -704,17 +704,23 @@ def w4a8_lora(X, Y, A, B, ids, scale=None, stream=None, flags=0):
         if ids.numel() != M:
             raise ValueError("%d ids for %d rows" % (ids.numel(), M))
         st = _together(stream, X, Y, A, B, scale, ids)
-        if M > LORA_IDS_MAX:
-            # (the second kernel may start early: it waits before it reads)
-            plan, ids = w4a8_lora_plan(ids, L, stream=stream, flags=flags), None
-            offsets, rows = plan.offsets, plan.rows
-            flags |= W4A8_FLAG_PDL
+    i_p = o_p = r_p = None
+    if offsets is not None:
+        o_p, r_p = offsets.data_ptr(), rows.data_ptr()
+    elif M <= LORA_IDS_MAX:
+        i_p = ids.data_ptr()
+    else:  # a plan for this call: offsets and rows in one buffer
+        buf = _new(stream, (L + 1 + M,), _torch.int32, X.device)
+        o_p = buf.data_ptr()
+        r_p = o_p + 4 * (L + 1)
+        rc = lib().w4a8_lora_plan(ids.data_ptr(), M, L, o_p, r_p, flags, st)
+        if rc:
+            _check(rc, "w4a8_lora_plan")
+        # (the second kernel may start early: it waits before it reads)
+        flags |= W4A8_FLAG_PDL
     rc = lib().w4a8_lora(X.data_ptr(), kind, ldx, M, K, A.data_ptr(), B.data_ptr(), r, L,
                          None if scale is None else scale.data_ptr(),
-                         None if ids is None else ids.data_ptr(),
-                         None if offsets is None else offsets.data_ptr(),
-                         None if rows is None else rows.data_ptr(), N, Y.data_ptr(), ldy,
-                         flags, st)
+                         i_p, o_p, r_p, N, Y.data_ptr(), ldy, flags, st)
     if rc:
         _check(rc, "w4a8_lora")
     return Y
