@@ -75,7 +75,14 @@ __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uin
 // The warps of a CTA: WR row groups of 16, WK blocks of 32 k (slices of 32
 // columns in the second product), WN parts of the rank tiles (of a slice's
 // columns).
-template <bool BF16X, int NT, int WR>
+// YV: rows of Y are 16-byte aligned; otherwise a row's stretch of Y comes in
+// the 16-byte granules that cover it (one more than its length asks for),
+// lanes read it from there at any 2-byte place, and it leaves through the
+// same place, 64 bytes of a row at a time (lanes that load and store their 8
+// columns element by element took 218 us for 4118 rows, 1408 x 6323, fp32 x,
+// rank 128, and 80 for 933 rows, 2432 x 7445, bf16 x, rank 16; this 136 and
+// 49).
+template <bool BF16X, int NT, int WR, bool YV>
 struct LoraCfg {
   static constexpr int kThreads = 256;
   static constexpr int kWarpsN = WR == 1 ? 2 : 1;
@@ -90,7 +97,7 @@ struct LoraCfg {
   static constexpr int kSlices = kWarpsK * (WR > 1 && NT <= 4 ? 2 : 1);
   static constexpr int max2(int a, int b) { return a > b ? a : b; }
   static constexpr int kXBytes =
-      kTileRows * max2(kBlocksK * (BF16X ? 64 : 128), kSlices * 64);
+      kTileRows * max2(kBlocksK * (BF16X ? 64 : 128), kSlices * 64 + (YV ? 0 : 16));
   static constexpr int kABytes = NT * 8 * 64 * max2(kBlocksK, kSlices);
   static constexpr int kStageBytes = kXBytes + kABytes;
   static constexpr int kPitch = NT * 8 + 4;  // floats per row of t
@@ -121,6 +128,12 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ unsigned short lds16(uint32_t addr) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return v;
 }
 
@@ -167,10 +180,10 @@ __device__ __forceinline__ int lora_tile(const LoraParams& p, int slot, int tid,
 }
 
 // NT: tiles of 8 ranks (ranks past p.rank are zero); WR: tiles of 16 rows.
-template <bool BF16X, int NT, int WR>
-__global__ void __launch_bounds__(LoraCfg<BF16X, NT, WR>::kThreads, LoraCfg<BF16X, NT, WR>::kResident)
+template <bool BF16X, int NT, int WR, bool YV>
+__global__ void __launch_bounds__(LoraCfg<BF16X, NT, WR, YV>::kThreads, LoraCfg<BF16X, NT, WR, YV>::kResident)
 lora_kernel(const LoraParams p) {
-  using C = LoraCfg<BF16X, NT, WR>;
+  using C = LoraCfg<BF16X, NT, WR, YV>;
   constexpr int TM = C::kTileRows, WK = C::kWarpsK, WN = C::kWarpsN, RP = C::kPitch;
   constexpr int NTHR = C::kThreads, S = C::kStages, BK = C::kBlocksK, BS = C::kSlices;
   extern __shared__ __align__(128) uint8_t lsm[];
@@ -279,6 +292,7 @@ lora_kernel(const LoraParams p) {
   // What a thread copies keeps its place from stage to stage, so the
   // addresses are found once and advance by a constant.
   constexpr int XC = BK * (BF16X ? 4 : 8), AC = BK * 4, YC = BS * 4;  // chunks of a row
+  constexpr int YG = YC + 1;  // granules of a row of Y (not YV)
   constexpr int XS = NTHR / XC, AS = NTHR / AC, YS = NTHR / YC;  // rows apart
   constexpr int XI = TM / XS, YI = TM / YS, RI = XI > YI ? XI : YI;
   static_assert(XI * XS == TM && YI * YS == TM && XS % 2 == 0 && AS % 2 == 0 && YS % 2 == 0,
@@ -324,7 +338,7 @@ lora_kernel(const LoraParams p) {
       }
       ap += AC * 16;
     } else if (ahead < n_a + n_b) {
-      if (ahead == n_a) {
+      if (YV && ahead == n_a) {
         rin = 0;
 #pragma unroll
         for (int i = 0; i < YI; ++i)
@@ -333,13 +347,34 @@ lora_kernel(const LoraParams p) {
       }
       const int n = (s0 + (ahead - n_a) * BS) * 32;
       const int cols = min(min(BS * 32, s1 * 32 - n), p.N - n);
-      if (ych * 8 + 8 <= cols && p.y_vec) {
+      if constexpr (YV) {
+        if (ych * 8 + 8 <= cols) {
 #pragma unroll
-        for (int i = 0; i < YI; ++i)
-          if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + yto + i * NTHR * 16, rp[i]);
+          for (int i = 0; i < YI; ++i)
+            if (WR > 1 || (rin >> i & 1)) cp_async16(st_in + yto + i * NTHR * 16, rp[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < YI; ++i) rp[i] += YC * 16;
+      } else {
+        // (granules that reach over an end of Y are read element by element)
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p.Y);
+        const uintptr_t hi = lo + ((size_t)(p.M - 1) * p.ldy + p.N) * 2;
+        for (int i = tid; i < TM * YG; i += NTHR) {
+          const int row = i / YG, m = toks[row];
+          if (m < 0) continue;
+          const uintptr_t a = lo + ((size_t)m * p.ldy + n) * 2;
+          const uintptr_t from = (a & ~(uintptr_t)15) + 16 * (i % YG);
+          if (from >= a + 2 * cols) continue;
+          if (from >= lo && from + 16 <= hi) {
+            cp_async16(st_in + i * 16, reinterpret_cast<const void*>(from));
+          } else {
+            for (int e = 0; e < 8; ++e)
+              if (from + 2 * e >= lo && from + 2 * e < hi)
+                sts16(st_in + i * 16 + 2 * e,
+                      *reinterpret_cast<const unsigned short*>(from + 2 * e));
+          }
+        }
       }
-#pragma unroll
-      for (int i = 0; i < YI; ++i) rp[i] += YC * 16;
       const int chunks = cols * rc;
 #pragma unroll
       for (int i = 0; i < (BS * 32 * NT + NTHR - 1) / NTHR; ++i) {
@@ -535,6 +570,12 @@ lora_kernel(const LoraParams p) {
   uint16_t* yrow[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) yrow[h] = p.Y + (size_t)max(tok[h], 0) * p.ldy;
+  // (not YV) where this lane's columns of its rows lie in a stage
+  uint32_t u_at[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    u_at[h] = (wr * 16 + g + 8 * h) * YG * 16 +
+              (((uint32_t)(reinterpret_cast<uintptr_t>(yrow[h]) >> 1) & 7) + wk * 32 + ycol) * 2;
 #pragma unroll 1
   for (int s_at = s0 + wk; s_at < s0 + wk + n_b * BS; s_at += BS) {
     next();
@@ -543,13 +584,20 @@ lora_kernel(const LoraParams p) {
       const int sl = s_at + u * WK;
       if (sl >= s1) continue;
       const int col = sl * 32 + ycol;
-      const bool whole = p.y_vec && (col & ~7) + 8 <= p.N;
+      const bool whole = YV && (col & ~7) + 8 <= p.N;
       float d[QN][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[YW];
         const uint32_t at = st + y_at + u * WK * 64 + h * 8 * YC * 16;
-        if constexpr (YW == 4) {
+        if constexpr (!YV) {
+          const uint32_t o = st + u_at[h] + u * WK * 64;
+          uint32_t x[YW + 1];
+#pragma unroll
+          for (int q = 0; q <= YW; ++q) x[q] = lds32((o & ~3u) + 4 * q);
+#pragma unroll
+          for (int q = 0; q < YW; ++q) w[q] = __funnelshift_r(x[q], x[q + 1], (o & 2) * 8);
+        } else if constexpr (YW == 4) {
           const uint4 v = lds128(at);
           w[0] = v.x;
           w[1] = v.y;
@@ -560,7 +608,7 @@ lora_kernel(const LoraParams p) {
           w[0] = v.x;
           w[1] = v.y;
         }
-        if (!whole) {
+        if (YV && !whole) {
 #pragma unroll
           for (int q = 0; q < YW; ++q) {
             w[q] = 0;
@@ -609,10 +657,16 @@ lora_kernel(const LoraParams p) {
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (tok[h] < 0) continue;
+        if (YV && tok[h] < 0) continue;
         uint32_t w[YW];
 #pragma unroll
         for (int q = 0; q < QN; ++q) w[q] = pack_bf16(d[q][2 * h], d[q][2 * h + 1]);
+        if constexpr (!YV) {
+#pragma unroll
+          for (int i = 0; i < CW; ++i)
+            sts16(st + u_at[h] + u * WK * 64 + 2 * i, (unsigned short)(w[i / 2] >> (16 * (i & 1))));
+          continue;
+        }
         uint16_t* yp = yrow[h] + col;
         if (whole) {
           if constexpr (YW == 4)
@@ -623,6 +677,19 @@ lora_kernel(const LoraParams p) {
 #pragma unroll
           for (int i = 0; i < CW; ++i)
             if (col + i < p.N) yp[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        }
+      }
+      if constexpr (!YV) {  // a row's 64 bytes (or two rows' 32) at a time
+        __syncwarp();
+        constexpr int CN = 32 / WN;
+        const int cc = lane % CN, to = sl * 32 + wn * CN + cc;
+#pragma unroll
+        for (int i = 0; i < 16; i += WN) {
+          const int r = wr * 16 + i + lane / CN, m = toks[r];
+          if (m < 0 || to >= p.N) continue;
+          uint16_t* y = p.Y + (size_t)m * p.ldy;
+          const int shift = (int)(reinterpret_cast<uintptr_t>(y) >> 1) & 7;
+          y[to] = lds16(st + r * YG * 16 + (shift + (u * WK + wk) * 32 + wn * CN + cc) * 2);
         }
       }
     }

@@ -1013,23 +1013,28 @@ cudaError_t launch_combine(const uint16_t* Y, int rows, int N, const int* pos,
                   0, st, pdl, 1, Y, rows, N, pos, weights, top_k, out);
 }
 
-template <bool BF16X, int NT, int WR>
+template <bool BF16X, int NT, int WR, bool YV>
 cudaError_t launch_lora_as(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
+  using C = LoraCfg<BF16X, NT, WR, YV>;
   static std::atomic<bool> done[kMaxDevices];
-  constexpr int smem = LoraCfg<BF16X, NT, WR>::kSmemBytes;
-  const cudaError_t e = ensure_smem(lora_kernel<BF16X, NT, WR>, smem, done);
+  const cudaError_t e = ensure_smem(lora_kernel<BF16X, NT, WR, YV>, C::kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_k(lora_kernel<BF16X, NT, WR>, dim3(slots * p.ctas, parts),
-                  dim3(LoraCfg<BF16X, NT, WR>::kThreads), smem,
-                  st, pdl, p.ctas, p);
+  return launch_k(lora_kernel<BF16X, NT, WR, YV>, dim3(slots * p.ctas, parts), dim3(C::kThreads),
+                  C::kSmemBytes, st, pdl, p.ctas, p);
+}
+
+template <bool BF16X, int WR, bool YV>
+cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
+  if (p.rank <= 16) return launch_lora_as<BF16X, 2, WR, YV>(p, slots, parts, st, pdl);
+  if (p.rank <= 32) return launch_lora_as<BF16X, 4, WR, YV>(p, slots, parts, st, pdl);
+  if (p.rank <= 64) return launch_lora_as<BF16X, 8, WR, YV>(p, slots, parts, st, pdl);
+  return launch_lora_as<BF16X, 16, WR, YV>(p, slots, parts, st, pdl);
 }
 
 template <bool BF16X, int WR>
-cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
-  if (p.rank <= 16) return launch_lora_as<BF16X, 2, WR>(p, slots, parts, st, pdl);
-  if (p.rank <= 32) return launch_lora_as<BF16X, 4, WR>(p, slots, parts, st, pdl);
-  if (p.rank <= 64) return launch_lora_as<BF16X, 8, WR>(p, slots, parts, st, pdl);
-  return launch_lora_as<BF16X, 16, WR>(p, slots, parts, st, pdl);
+cudaError_t launch_lora_wr(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
+  return p.y_vec ? launch_lora_nt<BF16X, WR, true>(p, slots, parts, st, pdl)
+                 : launch_lora_nt<BF16X, WR, false>(p, slots, parts, st, pdl);
 }
 
 // Tensor map of a row-major bf16 matrix: boxes of 64 columns by `rows` rows,
@@ -1177,10 +1182,10 @@ cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool
   while (slots * ctas * parts * 4 <= sms && p.N >= 256 * ctas * parts) parts *= 2;
   p.ctas = ctas;
   if (tall)
-    return bf16x ? launch_lora_nt<true, 4>(p, slots, parts, st, pdl)
-                 : launch_lora_nt<false, 4>(p, slots, parts, st, pdl);
-  return bf16x ? launch_lora_nt<true, 1>(p, slots, parts, st, pdl)
-               : launch_lora_nt<false, 1>(p, slots, parts, st, pdl);
+    return bf16x ? launch_lora_wr<true, 4>(p, slots, parts, st, pdl)
+                 : launch_lora_wr<false, 4>(p, slots, parts, st, pdl);
+  return bf16x ? launch_lora_wr<true, 1>(p, slots, parts, st, pdl)
+               : launch_lora_wr<false, 1>(p, slots, parts, st, pdl);
 }
 
 __global__ void timeout_probe_kernel(unsigned long long limit_ns) {
