@@ -77,11 +77,12 @@ __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uin
 // columns).
 // YV: rows of Y are 16-byte aligned; otherwise a row's stretch of Y comes in
 // the 16-byte granules that cover it (one more than its length asks for),
-// lanes read it from there at any 2-byte place, and it leaves through the
-// same place, 64 bytes of a row at a time (lanes that load and store their 8
-// columns element by element took 218 us for 4118 rows, 1408 x 6323, fp32 x,
-// rank 128, and 80 for 933 rows, 2432 x 7445, bf16 x, rank 16; this 136 and
-// 49).
+// lanes read and write it there at any 2-byte place, and it leaves by the same
+// granules
+// (lanes that load and store their 8 columns element by element took 218 us
+// for 4118 rows, 1408 x 6323, fp32 x, rank 128, and 80 for 933 rows, 2432 x
+// 7445, bf16 x, rank 16; this 106 and 40.  Rows of 6328 and 7448 take 53, on
+// the tcgen05 form, and 25).
 template <bool BF16X, int NT, int WR, bool YV>
 struct LoraCfg {
   static constexpr int kThreads = 256;
@@ -295,7 +296,8 @@ lora_kernel(const LoraParams p) {
   constexpr int YG = YC + 1;  // granules of a row of Y (not YV)
   constexpr int XS = NTHR / XC, AS = NTHR / AC, YS = NTHR / YC;  // rows apart
   constexpr int XI = TM / XS, YI = TM / YS, RI = XI > YI ? XI : YI;
-  static_assert(XI * XS == TM && YI * YS == TM && XS % 2 == 0 && AS % 2 == 0 && YS % 2 == 0,
+  static_assert(XI * XS == TM && YI * YS == TM && XS % 2 == 0 && AS % 2 == 0 && YS % 2 == 0 &&
+                    YI <= 8 && TM <= NTHR,
                 "copies");
   const int xrow = tid / XC, xch = tid % XC, arow = tid / AC, ach = tid % AC;
   const int yrow0 = tid / YC, ych = tid % YC;
@@ -318,6 +320,34 @@ lora_kernel(const LoraParams p) {
             (row_of(i, xrow + i * XS) * p.ldx + 32 * kb0) * (BF16X ? 2 : 4) + xch * 16;
   const uint8_t* ap = reinterpret_cast<const uint8_t*>(A + (size_t)arow * p.K + 32 * kb0) + ach * 16;
   const uint8_t* bp = reinterpret_cast<const uint8_t*>(B + (size_t)32 * s0 * p.rank) + tid * 16;
+  // (not YV) a thread's granules: the ych-th of its rows' (in rp), the last of
+  // row tid; and by how many elements a row's first granule starts early
+  const uint8_t* y_last = nullptr;
+  uint32_t y_shift = 0;
+  int y_shift_last = 0;
+  const uint8_t* y_lo = reinterpret_cast<const uint8_t*>(p.Y);
+  const uint8_t* y_hi = y_lo + ((size_t)(p.M - 1) * p.ldy + p.N) * 2;
+  auto y_in = [&](uint32_t to, const uint8_t* from, int granule, int shift, int cols) {
+    if (granule * 8 >= shift + cols) return;
+    if (from >= y_lo && from + 16 <= y_hi) {
+      cp_async16(to, from);
+    } else {  // it reaches over an end of Y
+      for (int e = 0; e < 8; ++e)
+        if (from + 2 * e >= y_lo && from + 2 * e < y_hi)
+          sts16(to + 2 * e, reinterpret_cast<const unsigned short*>(from)[e]);
+    }
+  };
+  // elements lo to hi - 1 of a granule
+  auto y_out = [&](uint32_t from, const uint8_t* to, int lo, int hi) {
+    uint8_t* t = const_cast<uint8_t*>(to);
+    if (lo <= 0 && hi >= 8) {
+      *reinterpret_cast<uint4*>(t) = lds128(from);
+    } else {
+      for (int e = max(lo, 0); e < min(hi, 8); ++e)
+        reinterpret_cast<unsigned short*>(t)[e] = lds16(from + 2 * e);
+    }
+  };
+  uint4 y_carry = make_uint4(0, 0, 0, 0);  // row tid's last granule, of the stage before
   int ahead = 0;          // the next stage to copy,
   uint32_t st_in = ring;  // and where it goes
   auto issue = [&]() {
@@ -338,6 +368,22 @@ lora_kernel(const LoraParams p) {
       }
       ap += AC * 16;
     } else if (ahead < n_a + n_b) {
+      if (!YV && ahead == n_a) {
+        rin = 0;
+#pragma unroll
+        for (int i = 0; i < YI; ++i) {
+          const uintptr_t a = reinterpret_cast<uintptr_t>(
+              p.Y + row_of(i, yrow0 + i * YS) * p.ldy + 32 * s0);
+          rp[i] = reinterpret_cast<const uint8_t*>(a & ~(uintptr_t)15) + ych * 16;
+          y_shift |= (uint32_t)(a >> 1 & 7) << (4 * i);
+        }
+        if (tid < TM) {
+          const uintptr_t a =
+              reinterpret_cast<uintptr_t>(p.Y + (size_t)max(toks[tid], 0) * p.ldy + 32 * s0);
+          y_last = reinterpret_cast<const uint8_t*>(a & ~(uintptr_t)15) + YC * 16;
+          y_shift_last = (int)(a >> 1 & 7);
+        }
+      }
       if (YV && ahead == n_a) {
         rin = 0;
 #pragma unroll
@@ -356,24 +402,14 @@ lora_kernel(const LoraParams p) {
 #pragma unroll
         for (int i = 0; i < YI; ++i) rp[i] += YC * 16;
       } else {
-        // (granules that reach over an end of Y are read element by element)
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p.Y);
-        const uintptr_t hi = lo + ((size_t)(p.M - 1) * p.ldy + p.N) * 2;
-        for (int i = tid; i < TM * YG; i += NTHR) {
-          const int row = i / YG, m = toks[row];
-          if (m < 0) continue;
-          const uintptr_t a = lo + ((size_t)m * p.ldy + n) * 2;
-          const uintptr_t from = (a & ~(uintptr_t)15) + 16 * (i % YG);
-          if (from >= a + 2 * cols) continue;
-          if (from >= lo && from + 16 <= hi) {
-            cp_async16(st_in + i * 16, reinterpret_cast<const void*>(from));
-          } else {
-            for (int e = 0; e < 8; ++e)
-              if (from + 2 * e >= lo && from + 2 * e < hi)
-                sts16(st_in + i * 16 + 2 * e,
-                      *reinterpret_cast<const unsigned short*>(from + 2 * e));
-          }
-        }
+        const uint32_t off = (uint32_t)(ahead - n_a) * (YC * 16);
+#pragma unroll
+        for (int i = 0; i < YI; ++i)
+          if (rin >> i & 1)
+            y_in(st_in + ((yrow0 + i * YS) * YG + ych) * 16, rp[i] + off, ych,
+                 y_shift >> (4 * i) & 7, cols);
+        if (tid < TM && toks[tid] >= 0)
+          y_in(st_in + (tid * YG + YC) * 16, y_last + off, YC, y_shift_last, cols);
       }
       const int chunks = cols * rc;
 #pragma unroll
@@ -662,9 +698,17 @@ lora_kernel(const LoraParams p) {
 #pragma unroll
         for (int q = 0; q < QN; ++q) w[q] = pack_bf16(d[q][2 * h], d[q][2 * h + 1]);
         if constexpr (!YV) {
+          const uint32_t o = st + u_at[h] + u * WK * 64;
+          if (o & 2) {
+            sts16(o, (unsigned short)w[0]);
 #pragma unroll
-          for (int i = 0; i < CW; ++i)
-            sts16(st + u_at[h] + u * WK * 64 + 2 * i, (unsigned short)(w[i / 2] >> (16 * (i & 1))));
+            for (int q = 0; q + 1 < YW; ++q)
+              sts32(o + 2 + 4 * q, __funnelshift_r(w[q], w[q + 1], 16));
+            sts16(o + 4 * YW - 2, (unsigned short)(w[YW - 1] >> 16));
+          } else {
+#pragma unroll
+            for (int q = 0; q < YW; ++q) sts32(o + 4 * q, w[q]);
+          }
           continue;
         }
         uint16_t* yp = yrow[h] + col;
@@ -679,18 +723,39 @@ lora_kernel(const LoraParams p) {
             if (col + i < p.N) yp[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
         }
       }
-      if constexpr (!YV) {  // a row's 64 bytes (or two rows' 32) at a time
-        __syncwarp();
-        constexpr int CN = 32 / WN;
-        const int cc = lane % CN, to = sl * 32 + wn * CN + cc;
+    }
+    if constexpr (!YV) {
+      // The stage's granules leave as they came.  A row's last one is the
+      // first of its next stage, which finds the columns that are done here
+      // in y_carry: only the ends of the CTA's stretch go by elements.
+      __syncthreads();
+      const int n = (s_at - wk) * 32;
+      const uint32_t off = (uint32_t)(s_at - wk - s0) * 64;
+      const int cols = min(min(BS * 32, s1 * 32 - n), p.N - n);
+      if (ych > 0) {
 #pragma unroll
-        for (int i = 0; i < 16; i += WN) {
-          const int r = wr * 16 + i + lane / CN, m = toks[r];
-          if (m < 0 || to >= p.N) continue;
-          uint16_t* y = p.Y + (size_t)m * p.ldy;
-          const int shift = (int)(reinterpret_cast<uintptr_t>(y) >> 1) & 7;
-          y[to] = lds16(st + r * YG * 16 + (shift + (u * WK + wk) * 32 + wn * CN + cc) * 2);
+        for (int i = 0; i < YI; ++i)
+          if (toks[yrow0 + i * YS] >= 0)
+            y_out(st + ((yrow0 + i * YS) * YG + ych) * 16, rp[i] + off, 0,
+                  (int)(y_shift >> (4 * i) & 7) + cols - ych * 8);
+      }
+      if (tid < TM && toks[tid] >= 0) {
+        const uint32_t row = st + tid * YG * 16;
+        const int ys = y_shift_last;
+        if (off > 0) {
+          auto pick = [&](uint32_t was, uint32_t is, int e) {  // elements e and e + 1
+            const uint32_t m = ys > e + 1 ? 0xffffffffu : ys > e ? 0xffffu : 0u;
+            return (was & m) | (is & ~m);
+          };
+          const uint4 v = lds128(row);
+          sts128(row, make_uint4(pick(y_carry.x, v.x, 0), pick(y_carry.y, v.y, 2),
+                                 pick(y_carry.z, v.z, 4), pick(y_carry.w, v.w, 6)));
         }
+        y_out(row, y_last + off - YC * 16, off > 0 ? 0 : ys, ys + cols);
+        if (s_at - wk + BS < s1)
+          y_carry = lds128(row + YC * 16);
+        else
+          y_out(row + YC * 16, y_last + off, 0, ys + cols - YC * 8);
       }
     }
     done();

@@ -127,6 +127,30 @@ def test_lora_strides_of_many_rows(dtype):
         assert torch.equal(big.view(torch.int16), before.view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K,N,r,L", [
+    (1, 128, 20011, 8, 1), (40, 256, 5003, 16, 3), (300, 128, 2501, 128, 2), (700, 128, 1237, 40, 20),
+    (3300, 128, 701, 16, 5), (3300, 128, 515, 128, 2), (700, 128, 5, 16, 4)])
+def test_lora_rows_that_begin_anywhere(M, K, N, r, L, dtype):
+    """Dense rows of odd length: they begin at every place of 16 bytes, each
+    next to rows that other tiles write; the bytes before the first and
+    behind the last stay."""
+    A, B, scale = _weights(L, K, N, r, M + N)
+    X = wl.random_matrix(M, K, M + 1).to(dtype).cuda()
+    ids = _ids(M, L, M + 2, False)
+    if M == 1:
+        ids[:] = 0
+    d = torch.from_numpy(ids).cuda()
+    flat = wl.random_matrix(1, M * N + 16, 18).bfloat16().cuda().view(-1)
+    before = flat.clone()
+    for y0 in range(8):
+        Y, Y0 = (t[y0:y0 + M * N].view(M, N) for t in (flat, before))
+        w4.w4a8_lora(X, Y, A, B, d, scale=scale)
+        check(Y0, Y, X, A, B, ids, scale)
+        Y.copy_(Y0)
+        assert torch.equal(flat.view(torch.int16), before.view(torch.int16))
+
+
 def test_lora_tensor_core_form_gives_up_cleanly():
     """With a wait budget of 0 the call stores nothing and the status says so;
     the next call works."""
