@@ -1013,45 +1013,6 @@ cudaError_t launch_combine(const uint16_t* Y, int rows, int N, const int* pos,
                   0, st, pdl, 1, Y, rows, N, pos, weights, top_k, out);
 }
 
-template <bool BF16X, int NT, int WR, bool YV>
-cudaError_t launch_lora_as(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
-  using C = LoraCfg<BF16X, NT, WR, YV>;
-  static std::atomic<bool> done[kMaxDevices];
-  const cudaError_t e = ensure_smem(lora_kernel<BF16X, NT, WR, YV>, C::kSmemBytes, done);
-  if (e != cudaSuccess) return e;
-  return launch_k(lora_kernel<BF16X, NT, WR, YV>, dim3(slots * p.ctas, parts), dim3(C::kThreads),
-                  C::kSmemBytes, st, pdl, p.ctas, p);
-}
-
-template <bool BF16X, int WR, bool YV>
-cudaError_t launch_lora_nt(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
-  if (p.rank <= 16) return launch_lora_as<BF16X, 2, WR, YV>(p, slots, parts, st, pdl);
-  if (p.rank <= 32) return launch_lora_as<BF16X, 4, WR, YV>(p, slots, parts, st, pdl);
-  if (p.rank <= 64) return launch_lora_as<BF16X, 8, WR, YV>(p, slots, parts, st, pdl);
-  return launch_lora_as<BF16X, 16, WR, YV>(p, slots, parts, st, pdl);
-}
-
-template <bool BF16X, int WR>
-cudaError_t launch_lora_wr(const LoraParams& p, int slots, int parts, cudaStream_t st, bool pdl) {
-  return p.y_vec ? launch_lora_nt<BF16X, WR, true>(p, slots, parts, st, pdl)
-                 : launch_lora_nt<BF16X, WR, false>(p, slots, parts, st, pdl);
-}
-
-// Tensor map of a row-major bf16 matrix: boxes of 64 columns by `rows` rows,
-// 128-byte swizzle, zero fill outside.
-bool make_bf16_map(CUtensorMap* map, const uint16_t* base, int cols, long long rows,
-                   int box_rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides,
-            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Clusters of `ctas` CTAs of a kernel that the machine holds at once (GPCs
 // do not divide evenly), asked once per device.
 template <typename F>
@@ -1078,6 +1039,81 @@ int clusters_at_once(F* kernel, int ctas, int threads, size_t smem, int sms,
   }
   cache[dev][ctas].store(n, std::memory_order_relaxed);
   return n;
+}
+
+// Tiles of 16 rows: how many CTAs share a tile's first product (a cluster) and
+// how many such clusters its columns, each of which repeats that product.  Of
+// the ways that the machine holds at once, the one whose CTAs read least of A
+// and B; a second wave costs more than any of them gains (17 rows of 17
+// adapters, 4096 x 12288, bf16 x, rank 16: 4 x 4, 272 CTAs, 9.7 us, 8 x 1 10.9,
+// 8 x 2, which do not fit, 14.1; 16 rows, rank 128: 4 x 2 19.0, 8 x 1, which do
+// not fit, 31.4; 32 rows, 8192 x 10240, rank 64: 8 x 1 18, 4 x 1 21, 2 x 1 35).
+// A CTA keeps 256 k.  Columns are divided up to 64 CTAs or so (1 row, 4096 x
+// 12288, rank 16: 6.2 us with 64, 7.5 with 16, 6.7 with 128), beyond that only
+// if a CTA keeps 384 (rank 64, 8 rows, 4096 x 12288: 9.6 us with 256 CTAs, 11.7
+// with 64; 12 rows, 4096 x 6000: 10.0 with 192, 375 columns each, 9.3 with 96).
+template <typename F>
+void split_tiles(F* kernel, int threads, size_t smem, int slots, int sms,
+                 std::atomic<int> (*room)[9], LoraParams& p, int& parts) {
+  double best = 1e30;
+  for (int c = 1; c <= 8 && (c == 1 || p.K >= 256 * c); c *= 2) {
+    const int at_once = clusters_at_once(kernel, c, threads, smem, sms, room);
+    if (c > 1 && slots > at_once) break;
+    int some = 1, all = 1;
+    while ((long long)slots * c * some * 4 <= sms && p.N >= 256 * c * some) some *= 2;
+    while ((long long)slots * all * 2 <= at_once) all *= 2;
+    if (p.N / 384 >= c * all) some = all;
+    const double reads = (double)p.K / c + (double)p.N / (c * some);
+    if (reads < best) {
+      best = reads;
+      p.ctas = c;
+      parts = some;
+    }
+  }
+}
+
+template <bool BF16X, int NT, int WR, bool YV>
+cudaError_t launch_lora_as(LoraParams p, int slots, int sms, cudaStream_t st, bool pdl) {
+  using C = LoraCfg<BF16X, NT, WR, YV>;
+  static std::atomic<bool> done[kMaxDevices];
+  static std::atomic<int> room[kMaxDevices][9];
+  const cudaError_t e = ensure_smem(lora_kernel<BF16X, NT, WR, YV>, C::kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  int parts = 1;
+  if constexpr (WR == 1)
+    split_tiles(lora_kernel<BF16X, NT, WR, YV>, C::kThreads, C::kSmemBytes, slots, sms, room, p,
+                parts);
+  return launch_k(lora_kernel<BF16X, NT, WR, YV>, dim3(slots * p.ctas, parts), dim3(C::kThreads),
+                  C::kSmemBytes, st, pdl, p.ctas, p);
+}
+
+template <bool BF16X, int WR, bool YV>
+cudaError_t launch_lora_nt(const LoraParams& p, int slots, int sms, cudaStream_t st, bool pdl) {
+  if (p.rank <= 16) return launch_lora_as<BF16X, 2, WR, YV>(p, slots, sms, st, pdl);
+  if (p.rank <= 32) return launch_lora_as<BF16X, 4, WR, YV>(p, slots, sms, st, pdl);
+  if (p.rank <= 64) return launch_lora_as<BF16X, 8, WR, YV>(p, slots, sms, st, pdl);
+  return launch_lora_as<BF16X, 16, WR, YV>(p, slots, sms, st, pdl);
+}
+
+template <bool BF16X, int WR>
+cudaError_t launch_lora_wr(const LoraParams& p, int slots, int sms, cudaStream_t st, bool pdl) {
+  return p.y_vec ? launch_lora_nt<BF16X, WR, true>(p, slots, sms, st, pdl)
+                 : launch_lora_nt<BF16X, WR, false>(p, slots, sms, st, pdl);
+}
+
+// Tensor map of a row-major bf16 matrix: boxes of 64 columns by `rows` rows,
+// 128-byte swizzle, zero fill outside.
+bool make_bf16_map(CUtensorMap* map, const uint16_t* base, int cols, long long rows,
+                   int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Tiles of tm rows that M rows of `used` adapters likely make: half a tile per
@@ -1160,13 +1196,7 @@ int tall_cluster(const LoraParams& p, bool bf16x, double tiles, int at_once) {
 // Otherwise row tiles of 64 where adapters have 32 rows or more on average and
 // there are tiles enough to fill the machine (8192 rows, 8192 x 8192, rank 32:
 // 112 us against 144 with tiles of 16; 1024 rows, 4096 x 4096, bf16: 21
-// against 16), else of 16, whose cluster grows while the CTAs still fit the
-// machine at once (one more doubling is a second wave: 32 rows of 32
-// adapters, 8192 x 10240, rank 64, take 20 us with 256 CTAs, 30 with 512, 35
-// with 64), a CTA keeping 256 k.  With few tiles N is split further, which
-// repeats the first product: one row, 4096 x 12288: 8.1 us with 64 CTAs, 9.4
-// with 16, 11.2 with 8; but 8 tiles are best left at 64 CTAs (9.4 against
-// 10.8 with 256).
+// against 16), else of 16.
 cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool pdl) {
   const int used = p.adapters < p.M ? p.adapters : p.M;
   if (p.rank > 32 && p.M / used >= 64 && (long long)p.rank * p.M >= 131072 && !p.ids &&
@@ -1175,17 +1205,13 @@ cudaError_t launch_lora(LoraParams p, bool bf16x, int sms, cudaStream_t st, bool
   const bool tall = p.M / used >= 32 && p.M / 64 >= sms / 3;
   const int tm = tall ? 64 : 16;
   const int slots = (int)(((long long)p.M + (long long)used * (tm - 1)) / tm);
-  int ctas = 1, parts = 1;
-  const int fit = p.rank > 64 ? sms : 2 * sms;  // CTAs at once
-  while (ctas < 8 && (long long)slots * ctas * 2 <= fit && p.K >= 512 * ctas) ctas *= 2;
-  if (tall) ctas = tall_cluster(p, bf16x, likely_tiles(p.M, used, tm), fit);
-  while (slots * ctas * parts * 4 <= sms && p.N >= 256 * ctas * parts) parts *= 2;
-  p.ctas = ctas;
-  if (tall)
-    return bf16x ? launch_lora_wr<true, 4>(p, slots, parts, st, pdl)
-                 : launch_lora_wr<false, 4>(p, slots, parts, st, pdl);
-  return bf16x ? launch_lora_wr<true, 1>(p, slots, parts, st, pdl)
-               : launch_lora_wr<false, 1>(p, slots, parts, st, pdl);
+  if (tall) {
+    p.ctas = tall_cluster(p, bf16x, likely_tiles(p.M, used, tm), p.rank > 64 ? sms : 2 * sms);
+    return bf16x ? launch_lora_wr<true, 4>(p, slots, sms, st, pdl)
+                 : launch_lora_wr<false, 4>(p, slots, sms, st, pdl);
+  }
+  return bf16x ? launch_lora_wr<true, 1>(p, slots, sms, st, pdl)
+               : launch_lora_wr<false, 1>(p, slots, sms, st, pdl);
 }
 
 __global__ void timeout_probe_kernel(unsigned long long limit_ns) {

@@ -129,6 +129,21 @@ def test_lora_strides_of_many_rows(dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,K,N,r,L", [
+    (1, 256, 100000, 8, 2), (5, 2048, 14344, 32, 9), (16, 384, 28672, 16, 40), (16, 1024, 8200, 128, 40),
+    (17, 1024, 6201, 64, 40), (36, 512, 9000, 24, 60), (36, 128, 4096, 8, 60)])
+def test_lora_columns_divided_among_clusters(M, K, N, r, L, dtype):
+    """Few tiles and many columns: each tile's go to several clusters."""
+    A, B, scale = _weights(L, K, N, r, M + r)
+    X = wl.random_matrix(M, K, M + 3).to(dtype).cuda()
+    Y0 = wl.random_matrix(M, N, M + 4).bfloat16().cuda()
+    ids = np.random.RandomState(M).permutation(L)[:M].astype(np.int32)
+    Y = Y0.clone()
+    w4.w4a8_lora(X, Y, A, B, torch.from_numpy(ids).cuda(), scale=scale)
+    check(Y0, Y, X, A, B, ids, scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,K,N,r,L", [
     (1, 128, 20011, 8, 1), (40, 256, 5003, 16, 3), (300, 128, 2501, 128, 2), (700, 128, 1237, 40, 20),
     (3300, 128, 701, 16, 5), (3300, 128, 515, 128, 2), (700, 128, 5, 16, 4)])
 def test_lora_rows_that_begin_anywhere(M, K, N, r, L, dtype):
